@@ -56,7 +56,8 @@ enum mla_status {
   MLA_ERR_TIMEOUT = -7,    /* (device status) a bounded wait inside a kernel gave up       */
   MLA_ERR_CUDA = -8,       /* a CUDA runtime/driver call failed (device query, TMA encode) */
   MLA_ERR_UNSUPPORTED = -9, /* no sm_103a-class device is current                          */
-  MLA_ERR_INTERNAL = -10   /* (device status) a kernel found an internal invariant broken  */
+  MLA_ERR_INTERNAL = -10,  /* (device status) a kernel found an internal invariant broken  */
+  MLA_ERR_NO_PAGES = -11   /* (result of a pool entry) the pool has too few free pages      */
 };
 
 /* Flags (bitwise OR). */
@@ -252,6 +253,154 @@ int mla_paged_decode_noalloc(const void* q_nope, const void* q_pe, const void* c
  * scratch and returns MLA_OK, MLA_ERR_TIMEOUT or MLA_ERR_INTERNAL (as
  * mla_read_device_status does for a caller's workspace).  No counterpart on the pages. */
 int mla_noalloc_read_status(void* stream);
+
+/*
+ * Causal prefill of a chunk of new tokens over an FP8 KV cache: mla_paged_prefill's
+ * arguments and mask with the cache of mla_paged_decode_fp8 (every latent value read as
+ * the same BF16 number).  Chunks may be ragged, down to one token or none per request;
+ * rows of requests with fewer keys than queries that see no key get out = 0, lse = -inf.
+ * dims->total_q may be larger than qo_indptr[batch]: the rows behind the last request are
+ * left as they were.  A listed slot outside the cache is not a key.
+ *   workspace >= mla_workspace_bytes_prefill_fp8(dims) bytes, zero-filled before its first
+ *   use; besides the prefill's scratch it holds the call's keys as bf16 rows (1156 bytes
+ *   for each of dims->num_kv_indices).
+ */
+size_t mla_workspace_bytes_prefill_fp8(const mla_dims* dims);
+int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
+                          const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out,
+                          float* lse, const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags,
+                          void* stream);
+
+/*
+ * Rotary positions and the cache write, for the new tokens of a step.  With 32 pairs of
+ * elements (interleaved: elements 2i and 2i + 1; else elements i and i + 32) and
+ * angle = positions[axis(i)][t] * inv_freq[i], pair (a, b) of every query head of token t
+ * and of its key becomes (a cos - b sin, a sin + b cos), computed in float32 and rounded to
+ * bf16 once; angles keep their precision at any int32 position.  Pairs 0 .. section[0] - 1
+ * follow axis 0, the next section[1] axis 1, the rest axis 2 (text: one axis; images and
+ * video: time, height, width).
+ *   q_pe  [tokens, H, 64] bf16 with strides (H may be 0: no queries, q_pe and q_out unused)
+ *   ckv   [tokens, 512] bf16 latents, written as they are;  k_pe [tokens, 64] bf16, rotated
+ *   positions [num_axes, tokens] int32;  inv_freq [32] float32 (device)
+ *   slots [tokens] int32 token slots; a token whose slot is outside the cache is not
+ *         written (its query is rotated all the same).  Slots named by several tokens end
+ *         up with a mixture of those tokens' values: name a slot once.
+ *   q_out [tokens, H, 64] bf16, contiguous; may be q_pe itself if q_pe is contiguous
+ * Strides are in elements and multiples of 8; all tensor pointers 16-byte aligned
+ * (MLA_ERR_ALIGN).  MLA_ERR_DIMS if the sections do not add up to 32 pairs over num_axes
+ * axes.  One launch.
+ *
+ * The _fp8 form writes the 656-byte token of mla_paged_decode_fp8: per 128 latent values
+ * scale = amax / 448 over the finite ones (1 for a tile of zeros) and the E4M3 number
+ * nearest to the float32 quotient value / scale; a value that is not finite is written
+ * as E4M3's NaN.  The rope part stays bf16.
+ */
+typedef struct mla_rope_dims {
+  int32_t tokens;
+  int32_t num_qo_heads;  /* 0..128 */
+  int32_t num_axes;      /* 1..3 */
+  int32_t section[3];    /* pairs of each axis; the used ones sum to 32 */
+  int32_t interleaved;   /* 1: pairs (2i, 2i + 1); 0: pairs (i, i + 32) */
+  int32_t num_pages;
+  int32_t page_size;
+  int64_t q_stride_token, q_stride_head; /* elements */
+  int64_t ckv_stride, kpe_stride;        /* elements between tokens */
+} mla_rope_dims;
+
+int mla_rope_append(const void* q_pe, const void* ckv, const void* k_pe, const int32_t* positions,
+                    const float* inv_freq, const int32_t* slots, void* q_out, void* ckv_cache, void* kpe_cache,
+                    const mla_rope_dims* dims, void* stream);
+int mla_rope_append_fp8(const void* q_pe, const void* ckv, const void* k_pe, const int32_t* positions,
+                        const float* inv_freq, const int32_t* slots, void* q_out, void* kv_fp8,
+                        const mla_rope_dims* dims, void* stream);
+
+/*
+ * Cached tokens as contiguous bf16 rows: row i of ckv_out [n, 512] and kpe_out [n, 64] is
+ * the token in slots[i] (FP8: dequantised as mla_paged_decode_fp8 reads it); zeros where
+ * slots[i] is outside the cache.  count: optional device scalar (for instance
+ * kv_indptr + batch); rows at or past it are left as they were.  One launch.
+ */
+int mla_cache_gather(const void* ckv_cache, const void* kpe_cache, const int32_t* slots, int n,
+                     const int32_t* count, int num_pages, int page_size, void* ckv_out, void* kpe_out,
+                     void* stream);
+int mla_cache_gather_fp8(const void* kv_fp8, const int32_t* slots, int n, const int32_t* count, int num_pages,
+                         int page_size, void* ckv_out, void* kpe_out, void* stream);
+
+/*
+ * Page copies within a cache: for e < n the first tokens[e] slots (tokens NULL: the whole
+ * page) of page src[e] are copied to page dst[e].  An entry with a page outside the cache
+ * (the pool's lists are padded with -1) copies nothing.  count: optional device scalar;
+ * entries at or past it are not read.  No page may be the dst of two entries, or the dst
+ * of one and the src of another (the pool's lists never have that; such pages end up with
+ * a mixture).  Run it once for every layer's cache.  One launch.
+ */
+int mla_cache_copy_pages(void* ckv_cache, void* kpe_cache, const int32_t* src, const int32_t* dst,
+                         const int32_t* tokens, int n, const int32_t* count, int num_pages, int page_size,
+                         void* stream);
+int mla_cache_copy_pages_fp8(void* kv_fp8, const int32_t* src, const int32_t* dst, const int32_t* tokens, int n,
+                             const int32_t* count, int num_pages, int page_size, void* stream);
+
+/*
+ * The page pool: which pages belong to which sequence.  Three device arrays of the caller:
+ *   block_table [max_rows, max_blocks] int32 page ids in sequence order
+ *   seq_lens    [max_rows] int32 (0: an empty row)
+ *   ref_count   [num_pages] int32: how many rows hold the page; 0 = free
+ * A row's entries past its last page in use are neither read nor changed.  A new pool has
+ * seq_lens and ref_count zero.  A caller may hold pages of its own (a prefix kept for later)
+ * by adding to their ref_count.  The arrays are what mla_block_table_to_csr and
+ * mla_paged_decode_block_table take.  The calls are deterministic: pages are taken lowest
+ * id first in the order of the entries.
+ *
+ * mla_pages_extend: row rows[i] grows by new_tokens[i] >= 0 tokens.
+ *   results [n]: MLA_OK; MLA_ERR_BAD_INDEX (nothing changes) if the row is out of range or
+ *     named by an earlier entry, the count negative, the new length over max_blocks *
+ *     page_size, or the row's last, partly filled page shared with another row;
+ *     MLA_ERR_NO_PAGES (nothing changes) if the entry needs pages and the free pages do not
+ *     cover it together with all earlier valid entries
+ *   new_indptr [n + 1]: offsets of the granted tokens (refused entries add none), packed in
+ *     list order (the qo_indptr of a prefill)
+ *   slots [capacity]: their token slots (the slots of mla_rope_append); positions past
+ *     the last granted token get -1, tokens past the capacity are counted but not written
+ * mla_pages_fork: row children[i] (empty) becomes a copy of row parents[i]: full pages are
+ *   shared (ref_count + 1), a partly filled last page gets a page of its own, whose first
+ *   copy_tokens[i] slots are to be copied from page src[i] to dst[i] by
+ *   mla_cache_copy_pages for every cache (-1, -1, 0 where nothing is to be copied).
+ *   results [n]: as above; MLA_ERR_BAD_INDEX also for a child that is not empty, is its own
+ *   parent or is named by an earlier entry.  Lengths are read as they were before the call.
+ * mla_pages_free: rows[i] gives up its pages (ref_count - 1; its entries become -1) and is
+ *   empty.  Rows that are empty, out of range or listed twice are no error.  ref_count
+ *   never goes below 0.
+ * mla_pages_compact: with L live pages, the live pages with ids >= L move, in id order, to
+ *   the free ids < L, ascending; block_table and ref_count are updated.
+ *   counts [2]: L and the number of moves; src, dst [num_pages / 2]: the moves, for
+ *   mla_cache_copy_pages (and for renaming page ids kept elsewhere), padded with -1.
+ *
+ * n entries, all arrays int32 on the device, outputs as described.  workspace >=
+ * mla_workspace_bytes_pages(pool, n) bytes (compact: n = 0), 16-byte aligned; nothing in
+ * it carries over between calls.  Calls on the same pool or workspace must be ordered.
+ * MLA_ERR_DIMS: negative sizes, page_size < 1, max_blocks * page_size or num_pages *
+ * page_size over INT32_MAX.
+ */
+typedef struct mla_pool {
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* ref_count;
+  int32_t max_rows;
+  int32_t max_blocks;
+  int32_t num_pages;
+  int32_t page_size;
+} mla_pool;
+
+size_t mla_workspace_bytes_pages(const mla_pool* pool, int n);
+int mla_pages_extend(const mla_pool* pool, const int32_t* rows, const int32_t* new_tokens, int n,
+                     int32_t* new_indptr, int32_t* slots, long long capacity, int32_t* results, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int mla_pages_fork(const mla_pool* pool, const int32_t* parents, const int32_t* children, int n, int32_t* src,
+                   int32_t* dst, int32_t* copy_tokens, int32_t* results, void* workspace, size_t workspace_bytes,
+                   void* stream);
+int mla_pages_free(const mla_pool* pool, const int32_t* rows, int n, void* stream);
+int mla_pages_compact(const mla_pool* pool, int32_t* counts, int32_t* src, int32_t* dst, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Workspace bytes a call with these dims needs (0 on invalid dims).  With
  * dims->num_workers == 0 it queries the current device's SM count. */

@@ -21,7 +21,8 @@ MLA_VALIDATE = 1
 
 _STATUS = {0: "MLA_OK", -1: "MLA_ERR_NULL", -2: "MLA_ERR_DIMS", -3: "MLA_ERR_ALIGN",
            -4: "MLA_ERR_WORKSPACE", -5: "MLA_ERR_LAUNCH", -6: "MLA_ERR_BAD_INDEX",
-           -7: "MLA_ERR_TIMEOUT", -8: "MLA_ERR_CUDA", -9: "MLA_ERR_UNSUPPORTED", -10: "MLA_ERR_INTERNAL"}
+           -7: "MLA_ERR_TIMEOUT", -8: "MLA_ERR_CUDA", -9: "MLA_ERR_UNSUPPORTED", -10: "MLA_ERR_INTERNAL",
+           -11: "MLA_ERR_NO_PAGES"}
 
 
 class MlaError(RuntimeError):
@@ -36,6 +37,19 @@ class MlaDims(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("total_q", ctypes.c_int32), ("num_kv_indices", ctypes.c_int32),
                 ("num_workers", ctypes.c_int32)]
+
+
+class MlaRopeDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("num_qo_heads", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("section", ctypes.c_int32 * 3), ("interleaved", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("q_stride_token", ctypes.c_int64),
+                ("q_stride_head", ctypes.c_int64), ("ckv_stride", ctypes.c_int64), ("kpe_stride", ctypes.c_int64)]
+
+
+class MlaPool(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("ref_count", ctypes.c_void_p),
+                ("max_rows", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
 
 
 _lib = None
@@ -68,6 +82,24 @@ _SIGNATURES = [
       ctypes.c_int, _P]),
     ("mla_paged_decode_noalloc", ctypes.c_int,
      [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), ctypes.c_int, _P]),
+    ("mla_workspace_bytes_prefill_fp8", ctypes.c_size_t, [ctypes.POINTER(MlaDims)]),
+    ("mla_paged_prefill_fp8", ctypes.c_int,
+     [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P, ctypes.c_size_t, ctypes.c_int,
+      _P]),
+    ("mla_rope_append", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(MlaRopeDims), _P]),
+    ("mla_rope_append_fp8", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(MlaRopeDims), _P]),
+    ("mla_cache_gather", ctypes.c_int, [_P, _P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P]),
+    ("mla_cache_gather_fp8", ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P]),
+    ("mla_cache_copy_pages", ctypes.c_int,
+     [_P, _P, _P, _P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int, _P]),
+    ("mla_cache_copy_pages_fp8", ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int, _P]),
+    ("mla_workspace_bytes_pages", ctypes.c_size_t, [ctypes.POINTER(MlaPool), ctypes.c_int]),
+    ("mla_pages_extend", ctypes.c_int,
+     [ctypes.POINTER(MlaPool), _P, _P, ctypes.c_int, _P, _P, ctypes.c_longlong, _P, _P, ctypes.c_size_t, _P]),
+    ("mla_pages_fork", ctypes.c_int,
+     [ctypes.POINTER(MlaPool), _P, _P, ctypes.c_int, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("mla_pages_free", ctypes.c_int, [ctypes.POINTER(MlaPool), _P, ctypes.c_int, _P]),
+    ("mla_pages_compact", ctypes.c_int, [ctypes.POINTER(MlaPool), _P, _P, _P, _P, ctypes.c_size_t, _P]),
     ("mla_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(MlaDims), ctypes.c_int]),
     ("mla_workspace_bytes_mtp", ctypes.c_size_t, [ctypes.POINTER(MlaDims), ctypes.c_int]),
     ("mla_default_num_workers", ctypes.c_int, []),
@@ -599,3 +631,10 @@ def run_workload(w, out=None, lse=None, workspace=None, flags=0, num_workers=0, 
                                 w.sm_scale, out, lse, workspace, flags, num_workers, stream)
     return mla_paged_prefill(w.q_nope, w.q_pe, w.ckv_cache, w.kpe_cache, w.qo_indptr, w.kv_indptr,
                              w.kv_indices, w.sm_scale, out, lse, workspace, flags, num_workers, stream)
+
+
+# The cache's writers and readers, the FP8 chunk prefill and the page pool.
+from .cache import (mla_cache_copy_pages, mla_cache_copy_pages_fp8, mla_cache_gather,  # noqa: E402
+                    mla_cache_gather_fp8, mla_paged_prefill_fp8, mla_pages_compact, mla_pages_extend,
+                    mla_pages_fork, mla_pages_free, mla_rope_append, mla_rope_append_fp8, workspace_bytes_pages,
+                    workspace_bytes_prefill_fp8)

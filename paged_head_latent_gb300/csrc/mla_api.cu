@@ -406,6 +406,68 @@ bool block_table_dims(const mla_dims* dims, int max_blocks, mla_dims* d) {
 }
 }  // namespace
 
+namespace {
+// Workspace of the FP8 prefill: the prefill's own, then the call's keys as bf16 rows in list
+// order (a whole number of 64-key tiles) and their indices.
+struct PrefillFp8Layout {
+  size_t decode, ckv, kpe, index, total;
+  long long rows;
+  PrefillFp8Layout(size_t base, int num_kv_indices) {
+    rows = ((long long)num_kv_indices + mla::kTileKeys - 1) / mla::kTileKeys * mla::kTileKeys;
+    decode = mla::align_up(base, 256);
+    ckv = decode;
+    kpe = ckv + (size_t)rows * mla::kDimCkv * 2;
+    index = kpe + (size_t)rows * mla::kDimKpe * 2;
+    total = mla::align_up(index + (size_t)rows * sizeof(int32_t), 256);
+  }
+};
+}  // namespace
+
+extern "C" {
+
+size_t mla_workspace_bytes_prefill_fp8(const mla_dims* dims) {
+  const size_t base = mla_workspace_bytes(dims, 1);
+  return base == 0 ? 0 : PrefillFp8Layout(base, dims->num_kv_indices).total;
+}
+
+int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
+                          const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out, float* lse,
+                          const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream) {
+  const int dims_ok = check_dims(dims, true);
+  if (dims_ok != MLA_OK) return dims_ok;
+  if (dims->total_q == 0) return MLA_OK;
+  const size_t base = mla_workspace_bytes(dims, 1);
+  if (base == 0) return MLA_ERR_CUDA;
+  if (!q_nope || !q_pe || !qo_indptr || !kv_indptr || !out || !lse) return MLA_ERR_NULL;
+  if (dims->num_kv_indices > 0 && !kv_indices) return MLA_ERR_NULL;
+  if (dims->num_pages > 0 && !kv_fp8) return MLA_ERR_NULL;
+  const PrefillFp8Layout lay(base, dims->num_kv_indices);
+  if (!workspace || workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
+  if (!aligned16(workspace) || !aligned16(kv_fp8) || !aligned16(q_nope) || !aligned16(q_pe) || !aligned16(out))
+    return MLA_ERR_ALIGN;
+  auto* ws = static_cast<uint8_t*>(workspace);
+  mla_dims d = *dims;
+  d.page_size = mla::kTileKeys;
+  d.num_pages = dims->num_pages > 0 ? (int)(lay.rows / mla::kTileKeys) : 0;
+  if (d.num_pages > 0) {
+    mla::GatherParams g{};
+    g.kv_fp8 = static_cast<const uint8_t*>(kv_fp8);
+    g.slots = kv_indices;
+    g.count = kv_indptr + dims->batch;  // keys in use: num_kv_indices may be a capacity
+    g.ckv_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.ckv);
+    g.kpe_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.kpe);
+    g.index = reinterpret_cast<int32_t*>(ws + lay.index);
+    g.n = dims->num_kv_indices;
+    g.num_slots = dims->num_pages * dims->page_size;
+    if (mla::launch_gather(g, true, static_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
+  }
+  return run(true, 0, q_nope, q_pe, ws + lay.ckv, ws + lay.kpe, qo_indptr, kv_indptr,
+             reinterpret_cast<const int32_t*>(ws + lay.index), sm_scale, out, lse, &d, workspace, lay.decode, flags,
+             stream);
+}
+
+}  // extern "C"
+
 extern "C" {
 
 size_t mla_workspace_bytes_block_table(const mla_dims* dims, int max_blocks) {
@@ -470,6 +532,7 @@ const char* mla_status_string(int status) {
     case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT: a bounded wait in a kernel gave up";
     case MLA_ERR_CUDA: return "MLA_ERR_CUDA: a CUDA runtime call failed";
     case MLA_ERR_UNSUPPORTED: return "MLA_ERR_UNSUPPORTED: current device is not sm_103";
+    case MLA_ERR_NO_PAGES: return "MLA_ERR_NO_PAGES: the pool has too few free pages";
     case MLA_ERR_INTERNAL: return "MLA_ERR_INTERNAL: a kernel found an internal invariant broken (shared memory misaligned)";
     default: return "unknown mla_status";
   }

@@ -1,0 +1,332 @@
+// mla_pages.cu -- the page pool: which pages of the cache belong to which sequence.
+//
+// The pool is three device arrays that the caller owns: block_table [max_rows, max_blocks]
+// (page ids in sequence order), seq_lens [max_rows] and ref_count [num_pages] (how many
+// sequences hold a page; 0 = free).  There is no free list to keep consistent: a call that
+// needs pages takes the free pages with the lowest ids, in the order of its entries, so its
+// outcome is unique whatever the order of the kernels' threads, and the pages it fills lie
+// at the front of the cache.
+//
+// A call is a few launches on one stream: a bitmap of the free pages (one pass over
+// ref_count, 4 bytes a page), one block that numbers them and decides every entry, and a
+// grid that applies the decisions.  Nothing but integers is computed; the counters that
+// several threads change are changed by integer atomics, whose order does not matter.
+#include "launch.h"
+#include "mla_paged.h"
+
+namespace mla {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kApplyThreads = 128;
+
+__device__ __forceinline__ int blocks_of(int len, int page_size) {
+  return len <= 0 ? 0 : (len - 1) / page_size + 1;
+}
+
+// A row's blocks in use, clamped to the table.
+__device__ __forceinline__ int used_blocks(const PoolParams& p, int len) {
+  return min(blocks_of(len, p.page_size), p.max_blocks);
+}
+
+__device__ __forceinline__ bool is_page(const PoolParams& p, int page) { return page >= 0 && page < p.num_pages; }
+
+// Bit i of word w: page 32 w + i is free.
+__global__ void __launch_bounds__(256) free_bitmap_kernel(PoolParams p, uint32_t* bits) {
+  const int words = (p.num_pages + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  for (int w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < words; w += (gridDim.x * blockDim.x) >> 5) {
+    const int page = 32 * w + lane;
+    const unsigned b = __ballot_sync(0xffffffffu, page < p.num_pages && p.ref_count[page] <= 0);
+    if (lane == 0) bits[w] = b;
+  }
+}
+
+// Exclusive sum of v over the block; *total = the block's sum.
+__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    long long s = part[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    part[lane] = s;
+  }
+  __syncthreads();
+  const long long before = warp ? part[warp - 1] : 0;
+  *total = part[kPlanThreads / 32 - 1];
+  __syncthreads();
+  return before + incl - v;
+}
+
+// Free pages before every word; returns the number of free pages.
+__device__ __forceinline__ long long number_free(const PoolParams& p, const PoolWork& w, long long* part) {
+  const int words = (p.num_pages + 31) / 32;
+  long long run = 0, total;
+  for (int base = 0; base < words; base += kPlanThreads) {
+    const int i = base + threadIdx.x;
+    const long long c = i < words ? __popc(w.bits[i]) : 0;
+    const long long at = run + block_scan(c, part, &total);
+    if (i < words) w.before[i] = (int32_t)at;
+    run += total;
+  }
+  return run;
+}
+
+// The ids of the first `need` free pages, in order.
+__device__ __forceinline__ void list_free(const PoolParams& p, const PoolWork& w, long long need) {
+  const int words = (p.num_pages + 31) / 32;
+  for (int i = threadIdx.x; i < words; i += kPlanThreads) {
+    uint32_t b = w.bits[i];
+    for (long long r = w.before[i]; b && r < need; ++r, b &= b - 1) w.pages[r] = 32 * i + __ffs(b) - 1;
+  }
+}
+
+// One block: decides every entry in list order.  Entry i is valid if its indices are and no
+// earlier entry names its row; a valid entry is granted if it needs no page, or if the
+// pages that the valid entries up to and including it need are there.
+template <bool kFork>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolParams p, PoolWork w) {
+  __shared__ long long part[32];
+  const long long free_pages = number_free(p, w, part);
+  const int32_t* rows = kFork ? p.children : p.rows;
+  auto good_row = [&](int r) { return r >= 0 && r < p.max_rows; };
+  for (int i = threadIdx.x; i < p.n; i += kPlanThreads)
+    if (good_row(rows[i])) w.claim[rows[i]] = 0x7fffffff;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.n; i += kPlanThreads)
+    if (good_row(rows[i])) atomicMin(&w.claim[rows[i]], i);
+  __syncthreads();
+  const long long room = (long long)p.max_blocks * p.page_size;
+  long long need_run = 0, new_run = 0, taken = 0, total;
+  for (int base = 0; base < p.n; base += kPlanThreads) {
+    const int i = base + threadIdx.x;
+    bool ok = false;
+    int len = 0, add = 0, need = 0;
+    if (i < p.n && good_row(rows[i]) && w.claim[rows[i]] == i) {
+      const int row = rows[i];
+      if constexpr (kFork) {
+        const int parent = p.parents[i];
+        ok = good_row(parent) && parent != row && p.seq_lens[row] == 0;
+        if (ok) {
+          len = p.seq_lens[parent];
+          ok = len >= 0 && len <= room;
+        }
+        if (ok && len % p.page_size != 0) {
+          ok = is_page(p, p.block_table[(size_t)parent * p.max_blocks + len / p.page_size]);
+          need = 1;
+        }
+      } else {
+        len = p.seq_lens[row];
+        add = p.new_tokens[i];
+        ok = len >= 0 && add >= 0 && (long long)len + add <= room;
+        if (ok && add > 0 && len % p.page_size != 0) {
+          // The new tokens go on in the row's last page, which has to be its own.
+          const int page = p.block_table[(size_t)row * p.max_blocks + len / p.page_size];
+          ok = is_page(p, page) && p.ref_count[page] == 1;
+        }
+        if (ok) need = blocks_of(len + add, p.page_size) - blocks_of(len, p.page_size);
+      }
+      if (!ok) need = 0;
+    }
+    const long long first = need_run + block_scan(need, part, &total);
+    need_run += total;
+    const bool granted = ok && (need == 0 || first + need <= free_pages);
+    const long long at = new_run + block_scan(granted ? add : 0, part, &total);
+    new_run += total;
+    block_scan(granted ? need : 0, part, &total);
+    taken += total;
+    if (i < p.n) {
+      p.results[i] = granted ? MLA_OK : ok ? MLA_ERR_NO_PAGES : MLA_ERR_BAD_INDEX;
+      w.old_len[i] = granted ? len : -1;
+      w.first[i] = (int32_t)first;
+      if (!kFork) p.new_indptr[i] = (int32_t)at;
+    }
+  }
+  if (!kFork && threadIdx.x == 0) p.new_indptr[p.n] = (int32_t)new_run;
+  list_free(p, w, taken);
+}
+
+// One block per entry: the row's new blocks, their counts, and the new tokens' slots.
+__global__ void __launch_bounds__(kApplyThreads) extend_kernel(PoolParams p, PoolWork w) {
+  for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
+    const int len = w.old_len[i];
+    if (len < 0) continue;
+    const int row = p.rows[i], add = p.new_tokens[i];
+    int32_t* table = p.block_table + (size_t)row * p.max_blocks;
+    const int have = blocks_of(len, p.page_size), want = blocks_of(len + add, p.page_size);
+    const int32_t* pages = w.pages + w.first[i];
+    for (int k = have + threadIdx.x; k < want; k += kApplyThreads) {
+      const int page = pages[k - have];
+      table[k] = page;
+      p.ref_count[page] = 1;
+    }
+    const int last = have > 0 && len % p.page_size != 0 ? table[have - 1] : 0;
+    const long long at = p.new_indptr[i];
+    for (int k = threadIdx.x; at >= 0 && k < add && at + k < p.capacity; k += kApplyThreads) {
+      const int pos = len + k, block = pos / p.page_size;
+      const int page = block < have ? last : pages[block - have];
+      p.slots[at + k] = page * p.page_size + pos % p.page_size;
+    }
+    if (threadIdx.x == 0) p.seq_lens[row] = len + add;
+  }
+  // Slots past the granted tokens name no slot, so a write of that many tokens skips them.
+  for (long long k = (long long)p.new_indptr[p.n] + blockIdx.x * kApplyThreads + threadIdx.x; k < p.capacity;
+       k += (long long)gridDim.x * kApplyThreads)
+    p.slots[k] = -1;
+}
+
+// One block per pair: the parent's full pages are shared, its partial page is listed for copying.
+__global__ void __launch_bounds__(kApplyThreads) fork_kernel(PoolParams p, PoolWork w) {
+  for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
+    const int len = w.old_len[i];
+    int src = -1, dst = -1, tokens = 0;
+    if (len >= 0) {
+      const int32_t* from = p.block_table + (size_t)p.parents[i] * p.max_blocks;
+      int32_t* to = p.block_table + (size_t)p.children[i] * p.max_blocks;
+      const int full = len / p.page_size;
+      for (int k = threadIdx.x; k < full; k += kApplyThreads) {
+        const int page = from[k];
+        to[k] = page;
+        if (is_page(p, page)) atomicAdd(&p.ref_count[page], 1);
+      }
+      tokens = len - full * p.page_size;
+      if (tokens > 0) {
+        src = from[full];
+        dst = w.pages[w.first[i]];
+        if (threadIdx.x == 0) {
+          to[full] = dst;
+          p.ref_count[dst] = 1;
+        }
+      }
+      if (threadIdx.x == 0) p.seq_lens[p.children[i]] = len;
+    }
+    if (threadIdx.x == 0) {
+      p.src[i] = src;
+      p.dst[i] = dst;
+      p.copy_tokens[i] = tokens;
+    }
+  }
+}
+
+// One block per listed row.  The row's length is taken by an exchange, so a row that is
+// listed twice is freed once.
+__global__ void __launch_bounds__(kApplyThreads) free_kernel(PoolParams p) {
+  __shared__ int taken;
+  for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
+    const int row = p.rows[i];
+    if (row < 0 || row >= p.max_rows) continue;
+    __syncthreads();
+    if (threadIdx.x == 0) taken = atomicExch(&p.seq_lens[row], 0);
+    __syncthreads();
+    const int used = used_blocks(p, taken);
+    int32_t* table = p.block_table + (size_t)row * p.max_blocks;
+    for (int k = threadIdx.x; k < used; k += kApplyThreads) {
+      const int page = table[k];
+      table[k] = -1;
+      if (is_page(p, page) && atomicSub(&p.ref_count[page], 1) <= 0) atomicAdd(&p.ref_count[page], 1);
+    }
+  }
+}
+
+// Compaction.  With L live pages, the live pages with ids >= L move, in order, to the free
+// pages with ids < L: as many of the one as of the other.
+__device__ __forceinline__ int free_before(const PoolWork& w, int page) {
+  return w.before[page >> 5] + __popc(w.bits[page >> 5] & ((1u << (page & 31)) - 1u));
+}
+
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PoolParams p, PoolWork w) {
+  __shared__ long long part[32];
+  const int live = p.num_pages - (int)number_free(p, w, part);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.counts[0] = live;
+    p.counts[1] = live < p.num_pages ? free_before(w, live) : 0;  // no page is free: none moves
+  }
+}
+
+__global__ void __launch_bounds__(256) compact_list_kernel(PoolParams p, PoolWork w) {
+  const int live = p.counts[0], moves = p.counts[1];
+  const int tid = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
+  for (int page = tid; page < p.num_pages; page += step) {
+    const bool is_free = (w.bits[page >> 5] >> (page & 31)) & 1u;
+    if (page < live && is_free) p.dst[free_before(w, page)] = page;
+    if (page >= live && !is_free) p.src[page - free_before(w, page) - (live - moves)] = page;
+  }
+  for (int k = moves + tid; k < p.num_pages / 2; k += step) p.src[k] = p.dst[k] = -1;
+}
+
+__global__ void __launch_bounds__(256) compact_apply_kernel(PoolParams p, PoolWork w) {
+  const int live = p.counts[0], moves = p.counts[1];
+  const long long tid = blockIdx.x * blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
+  for (long long k = tid; k < moves; k += step) {
+    p.ref_count[p.dst[k]] = p.ref_count[p.src[k]];
+    p.ref_count[p.src[k]] = 0;
+  }
+  const long long cells = (long long)p.max_rows * p.max_blocks;
+  for (long long c = tid; c < cells; c += step) {
+    const int row = (int)(c / p.max_blocks), k = (int)(c - (long long)row * p.max_blocks);
+    if (k >= blocks_of(p.seq_lens[row], p.page_size)) continue;
+    const int page = p.block_table[c];
+    if (page < live || page >= p.num_pages || ((w.bits[page >> 5] >> (page & 31)) & 1u)) continue;
+    p.block_table[c] = p.dst[page - free_before(w, page) - (live - moves)];
+  }
+}
+
+int grid_of(long long threads, int block, int most) {
+  const long long g = (threads + block - 1) / block;
+  return (int)(g < 1 ? 1 : g > most ? most : g);
+}
+
+cudaError_t launch_bitmap(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
+  free_bitmap_kernel<<<grid_of(p.num_pages, 256, 1216), 256, 0, stream>>>(p, w.bits);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_pages_extend(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
+  cudaError_t e = launch_bitmap(p, w, stream);
+  if (e != cudaSuccess) return e;
+  plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(p, w);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  extend_kernel<<<p.n < 1 ? 1 : p.n < 4096 ? p.n : 4096, kApplyThreads, 0, stream>>>(p, w);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
+  cudaError_t e = launch_bitmap(p, w, stream);
+  if (e != cudaSuccess) return e;
+  plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(p, w);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  fork_kernel<<<p.n < 4096 ? p.n : 4096, kApplyThreads, 0, stream>>>(p, w);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_free(const PoolParams& p, cudaStream_t stream) {
+  free_kernel<<<p.n < 4096 ? p.n : 4096, kApplyThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
+  cudaError_t e = launch_bitmap(p, w, stream);
+  if (e != cudaSuccess) return e;
+  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, w);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  compact_list_kernel<<<grid_of(p.num_pages, 256, 1216), 256, 0, stream>>>(p, w);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  compact_apply_kernel<<<grid_of((long long)p.max_rows * p.max_blocks, 256, 1216), 256, 0, stream>>>(p, w);
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -41,7 +41,6 @@ struct GatherParams {
   const int32_t* count;      // device scalar: rows past it are left as they are (nullptr: n)
   __nv_bfloat16* ckv_out;    // [n, 512]
   __nv_bfloat16* kpe_out;    // [n, 64]
-  int32_t* index;            // [n] or nullptr: row i's index i, -1 where the slot is outside the cache
   int n, num_slots;
 };
 

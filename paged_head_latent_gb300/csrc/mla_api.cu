@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "mla_paged.h"
+#include "chunk.h"
 #include "common.cuh"
 #include "launch.h"
 #include "tc_kernel.h"
@@ -406,64 +407,93 @@ bool block_table_dims(const mla_dims* dims, int max_blocks, mla_dims* d) {
 }
 }  // namespace
 
-namespace {
-// Workspace of the FP8 prefill: the prefill's own, then the call's keys as bf16 rows in list
-// order (a whole number of 64-key tiles) and their indices.
-struct PrefillFp8Layout {
-  size_t decode, ckv, kpe, index, total;
-  long long rows;
-  PrefillFp8Layout(size_t base, int num_kv_indices) {
-    rows = ((long long)num_kv_indices + mla::kTileKeys - 1) / mla::kTileKeys * mla::kTileKeys;
-    decode = mla::align_up(base, 256);
-    ckv = decode;
-    kpe = ckv + (size_t)rows * mla::kDimCkv * 2;
-    index = kpe + (size_t)rows * mla::kDimKpe * 2;
-    total = mla::align_up(index + (size_t)rows * sizeof(int32_t), 256);
-  }
-};
-}  // namespace
-
 extern "C" {
 
 size_t mla_workspace_bytes_prefill_fp8(const mla_dims* dims) {
-  const size_t base = mla_workspace_bytes(dims, 1);
-  return base == 0 ? 0 : PrefillFp8Layout(base, dims->num_kv_indices).total;
+  if (check_dims(dims, true) != MLA_OK) return 0;
+  int G = 0;
+  if (resolve_workers(dims, &G) != MLA_OK) return 0;
+  return mla::ChunkLayout(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices).total;
 }
 
 int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
                           const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out, float* lse,
-                          const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream) {
-  const int dims_ok = check_dims(dims, true);
-  if (dims_ok != MLA_OK) return dims_ok;
-  if (dims->total_q == 0) return MLA_OK;
-  const size_t base = mla_workspace_bytes(dims, 1);
-  if (base == 0) return MLA_ERR_CUDA;
+                          const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream_ptr) {
+  int st = check_dims(dims, true);
+  if (st != MLA_OK) return st;
+  if (!std::isfinite(sm_scale)) return MLA_ERR_DIMS;
+  if (dims->total_q == 0 || dims->batch == 0) return MLA_OK;
   if (!q_nope || !q_pe || !qo_indptr || !kv_indptr || !out || !lse) return MLA_ERR_NULL;
   if (dims->num_kv_indices > 0 && !kv_indices) return MLA_ERR_NULL;
   if (dims->num_pages > 0 && !kv_fp8) return MLA_ERR_NULL;
-  const PrefillFp8Layout lay(base, dims->num_kv_indices);
+  if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(kv_fp8) || !aligned16(out)) return MLA_ERR_ALIGN;
+  int G = 0;
+  if ((st = resolve_workers(dims, &G)) != MLA_OK) return st;
+  const mla::ChunkLayout lay(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices);
+  // (a staged row is a tensor-map coordinate)
+  if (lay.tiles * mla::kChunkKeys >= (1LL << 31)) return MLA_ERR_DIMS;
   if (!workspace || workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
-  if (!aligned16(workspace) || !aligned16(kv_fp8) || !aligned16(q_nope) || !aligned16(q_pe) || !aligned16(out))
-    return MLA_ERR_ALIGN;
+  if (!aligned16(workspace)) return MLA_ERR_ALIGN;
+  DeviceInfo info;
+  if ((st = query_device(&info)) != MLA_OK) return st;
+  if (info.major != 10 || info.minor != 3) return MLA_ERR_UNSUPPORTED;
+
   auto* ws = static_cast<uint8_t*>(workspace);
-  mla_dims d = *dims;
-  d.page_size = mla::kTileKeys;
-  d.num_pages = dims->num_pages > 0 ? (int)(lay.rows / mla::kTileKeys) : 0;
-  if (d.num_pages > 0) {
-    mla::GatherParams g{};
-    g.kv_fp8 = static_cast<const uint8_t*>(kv_fp8);
-    g.slots = kv_indices;
-    g.count = kv_indptr + dims->batch;  // keys in use: num_kv_indices may be a capacity
-    g.ckv_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.ckv);
-    g.kpe_out = reinterpret_cast<__nv_bfloat16*>(ws + lay.kpe);
-    g.index = reinterpret_cast<int32_t*>(ws + lay.index);
-    g.n = dims->num_kv_indices;
-    g.num_slots = dims->num_pages * dims->page_size;
-    if (mla::launch_gather(g, true, static_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_LAUNCH;
+  mla::ChunkParams p{};
+  p.qo_indptr = qo_indptr;
+  p.kv_indptr = kv_indptr;
+  p.kv_indices = kv_indices;
+  p.kv_fp8 = static_cast<const uint8_t*>(kv_fp8);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.batch = dims->batch;
+  p.heads = dims->num_qo_heads;
+  p.total_q = dims->total_q;
+  p.num_slots = dims->num_pages * dims->page_size;
+  p.num_kv_indices = dims->num_kv_indices;
+  p.workers = G;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  p.starts = reinterpret_cast<mla::ChunkStart*>(ws + lay.starts);
+  p.first_block = reinterpret_cast<int32_t*>(ws + lay.first_block);
+  p.blocks = reinterpret_cast<mla::ChunkBlock*>(ws + lay.blocks);
+  p.flags = reinterpret_cast<uint32_t*>(ws + lay.flags);
+  p.ckv = reinterpret_cast<__nv_bfloat16*>(ws + lay.ckv);
+  p.kpe = reinterpret_cast<__nv_bfloat16*>(ws + lay.kpe);
+  p.part_lse = reinterpret_cast<float*>(ws + lay.part_lse);
+  p.part_o = reinterpret_cast<float*>(ws + lay.part_o);
+  p.tiles = (int)lay.tiles;
+  p.max_blocks = (int)lay.max_blocks;
+  p.wait_ns = g_wait_ns.load();
+  p.fault_skip_tile = g_fault_skip_tile.load();
+
+  mla::ChunkMaps maps{};
+  const uint64_t rows = (uint64_t)dims->total_q * dims->num_qo_heads, keys = (uint64_t)lay.tiles * mla::kChunkKeys;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const auto l256 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B, l128 = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+  if ((st = get_map(&maps.q_nope, q_nope, rows, 512, 64, 64, sw, l256)) != MLA_OK) return st;
+  if ((st = get_map(&maps.q_pe, q_pe, rows, 64, 64, 64, sw, l128)) != MLA_OK) return st;
+  if ((st = get_map(&maps.ckv, p.ckv, keys, 512, 64, 64, sw, l256)) != MLA_OK) return st;
+  if ((st = get_map(&maps.kpe, p.kpe, keys, 64, 64, 64, sw, l128)) != MLA_OK) return st;
+
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  cudaGetLastError();  // clear stale errors so the checks below see only ours
+  if (flags & MLA_VALIDATE) {
+    MlaParams v{};
+    v.qo_indptr = qo_indptr;
+    v.kv_indptr = kv_indptr;
+    v.kv_indices = kv_indices;
+    v.batch = dims->batch;
+    v.rows = dims->total_q;
+    v.num_slots = p.num_slots;
+    v.num_kv_indices = dims->num_kv_indices;
+    v.status = p.status;
+    if (mla::launch_validate(v, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
   }
-  return run(true, 0, q_nope, q_pe, ws + lay.ckv, ws + lay.kpe, qo_indptr, kv_indptr,
-             reinterpret_cast<const int32_t*>(ws + lay.index), sm_scale, out, lse, &d, workspace, lay.decode, flags,
-             stream);
+  if (mla::launch_chunk_stage(p, stream) != cudaSuccess || mla::launch_chunk(maps, p, stream) != cudaSuccess ||
+      mla::launch_chunk_merge(p, stream) != cudaSuccess)
+    return MLA_ERR_LAUNCH;
+  return MLA_OK;
 }
 
 }  // extern "C"

@@ -203,8 +203,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
 }
 
 // Tokens read by slot into contiguous bf16 rows, kTok tokens of a warp in flight.  Tokens
-// whose slot is outside the cache become zero rows (index -1 in `index`, when given:
-// index[i] = i for a token of the cache).
+// whose slot is outside the cache become zero rows.
 template <bool kFp8, int kTok>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) {
   const int lane = threadIdx.x & 31;
@@ -215,7 +214,6 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) 
     int mine = -1;
     if (lane < kTok && i0 + lane < n) mine = p.slots[i0 + lane];
     if (mine >= p.num_slots) mine = -1;
-    if (p.index && lane < kTok && i0 + lane < n) p.index[i0 + lane] = mine < 0 ? -1 : (int32_t)(i0 + lane);
     uint4 a[kTok], b[kTok], r[kTok];
     float sc[kTok];
 #pragma unroll

@@ -27,8 +27,9 @@
 // The tensor pipe's order is S(j+1), then O += P(j) V(j): the softmax of tile j runs while S(j+1)
 // is computed.
 //
-// Warps: 0-3 softmax and output (thread = TMEM lane: row lane % 64, keys or columns half
-// lane / 64), 4 loads Q and K, 5 loads V, 6 issues the products (leader SM only), 7 tensor memory.
+// Warps: 0-7 softmax and output (a thread has a row, a quarter of a tile's keys and a quarter of
+// the output's columns), 8 loads Q and K, 9 loads V, 10 issues the products (leader SM only), 11
+// tensor memory.
 #include <mutex>
 #include <type_traits>
 
@@ -41,31 +42,30 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSoftmax = 4;  // softmax warps
-constexpr int kKWarp = 4, kVWarp = 5, kMmaWarp = 6, kTmemWarp = 7;
+constexpr int kThreads = 384;
+constexpr int kSoftmax = 8;  // softmax warps
+constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kTmemWarp = 11;
 constexpr uint32_t kBox = 64 * 128;  // 64 rows x 64 bf16, 128-byte swizzle
 constexpr int kKBoxes = 9, kVBoxes = 8;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kKBoxes * kBox;
 constexpr uint32_t kOffV = kOffK + kKBoxes * kBox;
 constexpr uint32_t kOffP = kOffV + kVBoxes * kBox;
-constexpr uint32_t kOffRed = kOffP + 2 * kBox;       // [2][2][64] row maxima
-constexpr uint32_t kOffL = kOffRed + 2 * 2 * 64 * 4;  // [2][64] row sums
-constexpr uint32_t kOffBar = kOffL + 2 * 64 * 4;
-constexpr uint32_t kOffMisc = kOffBar + 512;
+constexpr uint32_t kOffRed = kOffP + 2 * kBox;        // [2][4][64] row maxima
+constexpr uint32_t kOffBar = kOffRed + 2 * 4 * 64 * 4;
+constexpr uint32_t kOffMisc = kOffBar + 256;
 constexpr uint32_t kSmem = kOffMisc + 16;
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled only when a row's maximum grows by more than 2^8
 
-// A commit or a wait on the issuing thread costs about 90 cycles, so K is handed over in three
-// groups of three chunks and V in its two key halves; the last group of a product is free when
-// the product is done, which S_FULL and PV_DONE tell already.
+// K is handed over in groups of chunks and V in its two key halves; the last group of a product
+// is free when the product is done, which S_FULL and PV_DONE tell already.
+constexpr uint32_t kGroup = 3, kKGroups = kKBoxes / kGroup;
 enum Bar : uint32_t {
-  K_FULL, K_EMPTY = K_FULL + 3, V_FULL = K_EMPTY + 2, V_EMPTY = V_FULL + 2, Q_FULL, S_FULL, P_FULL = S_FULL + 2, PV_DONE,
-  O_EMPTY, DRAIN, NUM_BARS
+  K_FULL, K_EMPTY = K_FULL + kKGroups, V_FULL = K_EMPTY + kKGroups - 1, V_EMPTY = V_FULL + 2, Q_FULL, S_FULL,
+  P_FULL = S_FULL + 2, PV_DONE, O_EMPTY, DRAIN, NUM_BARS
 };
-static_assert(NUM_BARS * 8 <= 512, "barrier area");
+static_assert(NUM_BARS * 8 <= 256, "barrier area");
 static_assert(kSmem <= 232448, "shared memory");
 
 struct Misc {
@@ -123,11 +123,12 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The two warps that share rows (w and w + 2) meet here; a warp that leaves the loop early has
-// seen (or raised) the abort flag and arrives once more, which releases its partner.
-__device__ __forceinline__ void pair_sync(int warp) { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory"); }
-__device__ __forceinline__ void pair_release(int warp) {
-  asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
+// The four warps that share rows meet here; a warp that leaves the loop early has seen (or
+// raised) the abort flag and arrives once more, which helps to release the others, each of
+// which then sees the flag and does the same.
+__device__ __forceinline__ void rows_sync(int warp) { asm volatile("bar.sync %0, 128;" ::"r"(1 + (warp & 1)) : "memory"); }
+__device__ __forceinline__ void rows_release(int warp) {
+  asm volatile("bar.arrive %0, 128;" ::"r"(1 + (warp & 1)) : "memory");
 }
 
 // A worker's tiles in order, segment by segment (a segment: tiles of one block).
@@ -155,10 +156,12 @@ struct Walk {
   }
   __device__ bool first() const { return t == at.t; }
   __device__ bool last() const { return t == t_end - 1; }
-  __device__ void advance() {
-    if (++t < t_end) return;
+  __device__ void next_segment() {
     at = ChunkStart{at.i + 1, 0};
     open();
+  }
+  __device__ void advance() {
+    if (++t == t_end) next_segment();
   }
 };
 
@@ -211,14 +214,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (is_k) {
           if (fault && (int)j == p.fault_skip_tile) break;  // (test of the give-up path: no more loads)
 #pragma unroll
-          for (uint32_t g = 0; g < 3 && ok; ++g) {
+          for (uint32_t g = 0; g < kKGroups && ok; ++g) {
             if (j > 0)
-              ok = g < 2 ? mbar_wait(bar(K_EMPTY + g), again, abort, p.status, kStatusTimeout, p.wait_ns)
-                         : mbar_wait(bar(S_FULL + again), ((j - 1) >> 1) & 1, abort, p.status, kStatusTimeout, p.wait_ns);
+              ok = g < kKGroups - 1 ? mbar_wait(bar(K_EMPTY + g), again, abort, p.status, kStatusTimeout, p.wait_ns)
+                                    : mbar_wait(bar(S_FULL + again), ((j - 1) >> 1) & 1, abort, p.status, kStatusTimeout, p.wait_ns);
             if (!ok) break;
-            if (rank == 0) mbar_arrive_expect_tx(bar(K_FULL + g), 6 * kBox);
+            if (rank == 0) mbar_arrive_expect_tx(bar(K_FULL + g), 2 * kGroup * kBox);
 #pragma unroll
-            for (int c = 3 * g; c < 3 * (int)g + 3; ++c)
+            for (int c = kGroup * g; c < (int)(kGroup * (g + 1)); ++c)
               tma_load_pair(base + kOffK + c * kBox, c < 8 ? &maps.ckv : &maps.kpe, c < 8 ? 64 * c : 0, row + 64 * rank,
                             leader(K_FULL + g));
           }
@@ -257,21 +260,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t issue = elect_one();
       bool good = true;
       auto wait = [&](uint32_t i, uint32_t parity) {
-        good &= mbar_wait<true>(bar(i), parity, abort, p.status, kStatusTimeout, p.wait_ns);
+        good &= mbar_wait(bar(i), parity, abort, p.status, kStatusTimeout, p.wait_ns);
         __syncwarp();
       };
       auto scores = [&](uint32_t j, auto buffer) {  // S of tile j
 #pragma unroll
-        for (uint32_t g = 0; g < 3; ++g) {
+        for (uint32_t g = 0; g < kKGroups; ++g) {
           wait(K_FULL + g, j & 1);
           tc_fence_after();
 #pragma unroll
-          for (uint32_t c = 3 * g; c < 3 * g + 3; ++c)
+          for (uint32_t c = kGroup * g; c < kGroup * (g + 1); ++c)
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
               mma2(issue, kColS + 64 * decltype(buffer)::value, q0 + c * (kBox / 16) + 2 * k, k0 + c * (kBox / 16) + 2 * k,
                    kIdescS, c + k > 0);
-          commit2(issue, bar(g < 2 ? K_EMPTY + g : S_FULL + decltype(buffer)::value));
+          commit2(issue, bar(g < kKGroups - 1 ? K_EMPTY + g : S_FULL + decltype(buffer)::value));
         }
       };
       auto output = [&](uint32_t j, bool first, uint32_t seg) {  // O += P V of tile j
@@ -290,19 +293,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           commit2(issue, bar(h ? PV_DONE : V_EMPTY));
         }
       };
-      uint32_t j = 0, seg = 0;
-      bool first = false;
-      for (Walk it(p, w); it.live; it.advance(), ++j) {
-        const bool f = it.first();
-        if (f) wait(Q_FULL, it.seg & 1);
-        if (j & 1) scores(j, std::integral_constant<uint32_t, 1>{});
-        else scores(j, std::integral_constant<uint32_t, 0>{});
-        if (j > 0) output(j - 1, first, seg);
-        first = f;
-        seg = it.seg;
-        if (!__all_sync(0xffffffffu, good)) break;
+      // Within a segment S(j + 1) goes before O(j); at its end O comes first, so that the output
+      // does not wait for the next block's Q.
+      uint32_t j = 0;
+      for (Walk it(p, w); it.live && __all_sync(0xffffffffu, good); it.next_segment()) {
+        const uint32_t n = it.t_end - it.t;
+        wait(Q_FULL, it.seg & 1);
+        for (uint32_t i = 0; i <= n; ++i) {
+          if (i < n) {
+            if ((j + i) & 1) scores(j + i, std::integral_constant<uint32_t, 1>{});
+            else scores(j + i, std::integral_constant<uint32_t, 0>{});
+          }
+          if (i > 0) output(j + i - 1, i == 1, it.seg);
+          if (!__all_sync(0xffffffffu, good)) break;
+        }
+        j += n;
       }
-      if (__all_sync(0xffffffffu, good) && j > 0) output(j - 1, first, seg);
       // Everything issued is done once this arrives.
       commit2(issue, bar(DRAIN));
       volatile int no_abort = 0;
@@ -311,12 +317,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kSoftmax && sound) {
     // ------------------------------------------------------------ softmax and output
-    const int half = warp >> 1, r = 32 * (warp & 1) + lane;
-    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    // This thread: row r of the SM's 64, keys 64 half + 32 part .. + 31 of a tile, and output
+    // columns 256 half + 128 part .. + 127.
+    const int half = (warp >> 1) & 1, part = warp >> 2, r = 32 * (warp & 1) + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     float* red = reinterpret_cast<float*>(smem + kOffRed);
-    float* lsum = reinterpret_cast<float*>(smem + kOffL);
-    const uint32_t mine = base + kOffP + half * kBox + r * 128;     // this thread's row of P
-    const uint32_t piece = base + kOffP + half * kBox + (warp & 1) * 32 * 128;  // this warp's 4 KB of P
+    const int quarter = 2 * half + part;
+    const uint32_t mine = base + kOffP + half * kBox + r * 128;  // this thread's row of P
+    const uint32_t piece = base + kOffP + half * kBox + (warp & 1) * 4096 + part * 2048;  // 2 KB of P for the output
+    const uint32_t col_s = tmem + lanes + kColS + 32 * part, col_o = tmem + lanes + kColO + 128 * part;
     const uint32_t p_full = leader(P_FULL), o_empty = leader(O_EMPTY);
     const float scale = p.scale_log2;
     float m_ref = 0.f, l = 0.f;
@@ -332,58 +341,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool first = it.first();
       const int local = it.blk.local0 + 64 * rank + r;  // row within its request
       if (first) seen = it.blk.seen + local / p.heads;
-      const uint4* fl = reinterpret_cast<const uint4*>(p.flags + (size_t)(it.blk.tile0 + it.t) * 8);
-      const uint2 keys = __ldg(reinterpret_cast<const uint2*>(fl) + half);
-      const uint2 odd = __ldg(reinterpret_cast<const uint2*>(fl + 1) + half);
+      const uint32_t* fl = p.flags + (size_t)(it.blk.tile0 + it.t) * 8 + quarter;
+      const uint32_t keys = __ldg(fl), odd = __ldg(fl + 4);
       if (!wait(S_FULL + (j & 1), (j >> 1) & 1)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t s0[32], s1[32];
-      tmem_ld32(tmem + lanes + kColS + 64 * (j & 1), s0);
-      tmem_ld32(tmem + lanes + kColS + 64 * (j & 1) + 32, s1);
+      uint32_t raw[32];
+      tmem_ld32(col_s + 64 * (j & 1), raw);
       tmem_ld_wait();
-      float s[64];
+      float s[32];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        s[k] = __uint_as_float(s0[k]);
-        s[k + 32] = __uint_as_float(s1[k]);
-      }
-      const int n = seen - it.t * kChunkKeys - 64 * half;  // keys of this thread's half that the row sees
-      const bool full = n >= 64 && (keys.x & keys.y) == 0xffffffffu && (odd.x | odd.y) == 0 && scale >= 0.f;
+      for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(raw[k]);
+      const int n = seen - it.t * kChunkKeys - 32 * quarter;  // keys of this thread's part that the row sees
+      const bool full = n >= 32 && keys == 0xffffffffu && odd == 0 && scale >= 0.f;
       if (!full) {
-        const uint32_t v0 = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-        const uint32_t v1 = n >= 64 ? 0xffffffffu : n <= 32 ? 0u : (1u << (n - 32)) - 1u;
-        const uint32_t k0 = keys.x & v0, k1 = keys.y & v1;
+        const uint32_t see = keys & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
         // (a staged key that is not finite is all zeros: its scores are finite, the row is NaN below)
-        if ((odd.x & k0) | (odd.y & k1)) l = __int_as_float(0x7fc00000);
+        if (odd & see) l = __int_as_float(0x7fc00000);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          s[k] = (k0 >> k) & 1u ? s[k] * scale : -INFINITY;
-          s[k + 32] = (k1 >> k) & 1u ? s[k + 32] * scale : -INFINITY;
-        }
+        for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1u ? s[k] * scale : -INFINITY;
       }
       float mx;
       {
         float m8[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          m8[k] = fmaxf(fmaxf(s[k], s[k + 8]), fmaxf(s[k + 16], s[k + 24]));
-          m8[k] = fmaxf(m8[k], fmaxf(fmaxf(s[k + 32], s[k + 40]), fmaxf(s[k + 48], s[k + 56])));
-        }
+        for (int k = 0; k < 8; ++k) m8[k] = fmaxf(fmaxf(s[k], s[k + 8]), fmaxf(s[k + 16], s[k + 24]));
 #pragma unroll
         for (int k = 0; k < 4; ++k) m8[k] = fmaxf(m8[k], m8[k + 4]);
         mx = fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3]));
       }
       if (full) mx *= scale;
-      red[((j & 1) * 2 + half) * 64 + r] = mx;
-      pair_sync(warp);
+      float* red_j = red + (j & 1) * 256 + r;
+      red_j[64 * quarter] = mx;
+      rows_sync(warp);
       if (aborted()) {
         ok = false;
         break;
       }
-      mx = fmaxf(mx, red[((j & 1) * 2 + (half ^ 1)) * 64 + r]);
+      mx = fmaxf(fmaxf(red_j[0], red_j[64]), fmaxf(red_j[128], red_j[192]));
       bool rescale = false;
       float alpha = 1.f;
       if (first) {
@@ -396,11 +393,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         rescale = true;
       }
       const float m = m_ref == -INFINITY ? 0.f : m_ref;
-      uint32_t pk[32];
+      uint32_t pk[16];
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       const float mul = full ? scale : 1.f;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < 16; ++k) {
         const float a = fast_exp2(fmaf(s[2 * k], mul, -m)), b = fast_exp2(fmaf(s[2 * k + 1], mul, -m));
         sum[k & 3] += a + b;
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);  // the tensor cores' operand type
@@ -415,19 +412,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
-          tmem_ld32(tmem + lanes + kColO + 32 * c, o);
+          tmem_ld32(col_o + 32 * c, o);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st32(tmem + lanes + kColO + 32 * c, o);
+          tmem_st32(col_o + 32 * c, o);
         }
         tmem_st_wait();
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((u ^ (r & 7)) << 4)), "r"(pk[4 * u]),
+      for (int u = 0; u < 4; ++u)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (((4 * part + u) ^ (r & 7)) << 4)), "r"(pk[4 * u]),
                      "r"(pk[4 * u + 1]), "r"(pk[4 * u + 2]), "r"(pk[4 * u + 3])
                      : "memory");
       fence_proxy_async_smem();
@@ -437,13 +434,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
       if (it.last()) {
         // Output: O / l to out, or a fragment to the workspace.
-        lsum[half * 64 + r] = l;
-        pair_sync(warp);
+        red_j = red + ((j + 1) & 1) * 256 + r;  // (the maxima there were read before the last meeting)
+        red_j[64 * quarter] = l;
+        rows_sync(warp);
         if (aborted()) {
           ok = false;
           break;
         }
-        const float total = l + lsum[(half ^ 1) * 64 + r];
+        const float total = (red_j[0] + red_j[64]) + (red_j[128] + red_j[192]);
+        rows_sync(warp);  // the next tile writes its maxima there
         if (!wait(PV_DONE, j & 1)) {
           ok = false;
           break;
@@ -454,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int in_block = 64 * rank + 32 * (warp & 1);  // first of this warp's rows
         const int slot = it.seg == 0 ? 0 : 1;
         const size_t frag = ((size_t)w * 2 + slot) * kChunkRows;
-        if (half == 0 && in_block + lane < it.blk.rows) {
+        if (quarter == 0 && in_block + lane < it.blk.rows) {
           if (whole)
             p.lse[(size_t)it.blk.row0 + in_block + lane] =
                 total == 0.f ? -INFINITY : fmaf(m_ref, 0.69314718055994531f, logf(total));
@@ -462,13 +461,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             p.part_lse[frag + in_block + lane] = total == 0.f ? -INFINITY : m_ref + log2f(total);
         }
         uint32_t o[2][32];
-        tmem_ld32(tmem + lanes + kColO, o[0]);
+        tmem_ld32(col_o, o[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {  // 32 columns at a time, the next ones under way
+        for (int c = 0; c < 4; ++c) {  // 32 columns at a time, the next ones under way
           uint32_t(&x)[32] = o[c & 1];
           tmem_ld_wait();
-          if (c < 7) {
-            tmem_ld32(tmem + lanes + kColO + 32 * (c + 1), o[(c + 1) & 1]);
+          if (c < 3) {
+            tmem_ld32(col_o + 32 * (c + 1), o[(c + 1) & 1]);
           } else {  // O is in registers: the next block's products may begin
             tc_fence_before();
             __syncwarp();
@@ -482,11 +481,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float a = __uint_as_float(x[8 * u + 2 * e]), b = __uint_as_float(x[8 * u + 2 * e + 1]);
-                const __nv_bfloat162 h = __floats2bfloat162_rn(inv == 0.f ? 0.f : a * inv, inv == 0.f ? 0.f : b * inv);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(a * inv, b * inv);
                 y[e] = *reinterpret_cast<const uint32_t*>(&h);
               }
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece + (c & 1) * 2048 + lane * 64 +
-                                                                            ((u ^ ((lane >> 1) & 3)) << 4)),
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)),
                            "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                            : "memory");
             }
@@ -497,32 +495,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint4 v;
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                           : "r"(piece + (c & 1) * 2048 + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4))
+                           : "r"(piece + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4))
                            : "memory");
               if (in_block + rr < it.blk.rows)
-                *reinterpret_cast<uint4*>(p.out + ((size_t)it.blk.row0 + in_block + rr) * kDimCkv + 256 * half + 32 * c +
-                                          8 * u) = v;
+                *reinterpret_cast<uint4*>(p.out + ((size_t)it.blk.row0 + in_block + rr) * kDimCkv + 256 * half + 128 * part +
+                                          32 * c + 8 * u) = v;
             }
+            __syncwarp();
           } else {
             // A fragment lies as [column / 4][row][4], so a store is 512 contiguous bytes.
-            float4* dst = reinterpret_cast<float4*>(p.part_o + frag * kDimCkv) + (64 * half + 8 * c) * kChunkRows +
+            float4* dst = reinterpret_cast<float4*>(p.part_o + frag * kDimCkv) + (64 * half + 32 * part + 8 * c) * kChunkRows +
                           in_block + lane;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               float4 y;
-              y.x = inv == 0.f ? 0.f : __uint_as_float(x[4 * u]) * inv;
-              y.y = inv == 0.f ? 0.f : __uint_as_float(x[4 * u + 1]) * inv;
-              y.z = inv == 0.f ? 0.f : __uint_as_float(x[4 * u + 2]) * inv;
-              y.w = inv == 0.f ? 0.f : __uint_as_float(x[4 * u + 3]) * inv;
+              y.x = __uint_as_float(x[4 * u]) * inv;
+              y.y = __uint_as_float(x[4 * u + 1]) * inv;
+              y.z = __uint_as_float(x[4 * u + 2]) * inv;
+              y.w = __uint_as_float(x[4 * u + 3]) * inv;
               dst[u * kChunkRows] = y;
             }
           }
         }
-        __syncwarp();
         l = 0.f;
       }
     }
-    if (!ok) pair_release(warp);
+    if (!ok) rows_release(warp);
   }
 
   // The merge may be scheduled; it waits for this grid's end before it reads anything.

@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkP
   const ChunkReq r = load_request(p, lo);
   const int key0 = (tile - r.tile0) * kChunkKeys;
   const int here = min(kChunkKeys, r.kv_len - key0);
-  if (here <= 0 || key0 < 0 || r.q_len == 0) return;
+  // (a request without keys has one tile of zeros: its rows' weights are zero)
+  if ((here <= 0 && key0 != 0) || key0 < 0 || r.q_len == 0) return;
   if (threadIdx.x < 8) flags[threadIdx.x] = 0;
   __syncthreads();
   constexpr int kTok = 4;  // tokens of a warp in flight

@@ -15,123 +15,131 @@ import torch
 from . import (FP8_TOKEN_BYTES, HEAD_DIM_CKV, HEAD_DIM_KPE, MlaDims, MlaError, MlaPool, MlaRopeDims, _cache_geometry,
                lib, make_dims)
 
-_NULL = ctypes.c_void_p(None)
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_entry = {}
 
 
-def _check(name, t, dtype, dev=None, contiguous=True):
+def _check(name, t, dtype, index=None, contiguous=True):
+    """Raise unless ``t`` is a (contiguous) CUDA tensor of ``dtype`` on device ``index``.
+    The conditions that hold for every good argument are tested first and together: these
+    calls take a few microseconds on the GPU, and so should their checks."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and (not contiguous or t.is_contiguous())
+            and (index is None or t.get_device() == index)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _at(t: Optional[torch.Tensor]):
-    return _NULL if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _call(name, dev, stream, *args):
-    """The library's ``name`` on ``dev`` and ``stream`` (the last argument of every call)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    handle = ctypes.c_void_p(stream.cuda_stream)
-    if torch.cuda.current_device() == dev.index:
-        st = getattr(lib(), name)(*args, handle)
+def _call(name, index, stream, *args):
+    """The library's ``name`` on device ``index`` and ``stream`` (the last argument of every call)."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            st = getattr(lib(), name)(*args, handle)
+        with torch.cuda.device(index):
+            st = fn(*args, raw)
     if st != 0:
         raise MlaError(st, name)
 
 
-def _bf16_caches(ckv_cache, kpe_cache, dev=None):
-    _check("ckv_cache", ckv_cache, torch.bfloat16, dev)
-    _check("kpe_cache", kpe_cache, torch.bfloat16, ckv_cache.device)
+def _bf16_caches(ckv_cache, kpe_cache, index=None):
+    _check("ckv_cache", ckv_cache, _BF16, index)
+    _check("kpe_cache", kpe_cache, _BF16, ckv_cache.get_device())
     return _cache_geometry(ckv_cache, kpe_cache)
 
 
-def _fp8_cache(kv_fp8, dev=None):
-    _check("kv_fp8", kv_fp8, torch.uint8, dev)
+def _fp8_cache(kv_fp8, index=None):
+    _check("kv_fp8", kv_fp8, _U8, index)
     if kv_fp8.dim() != 3 or kv_fp8.shape[2] != FP8_TOKEN_BYTES:
         raise ValueError("kv_fp8 must be [num_pages, page_size, 656] uint8")
     return kv_fp8.shape[0], kv_fp8.shape[1]
 
 
-def _ints(name, t, shape, dev):
-    _check(name, t, torch.int32, dev)
-    if tuple(t.shape) != tuple(shape):
+def _ints(name, t, shape, index):
+    _check(name, t, _I32, index)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} int32, got {list(t.shape)}")
 
 
-def _buffer(name, t, shape, dtype, dev):
-    """``t``, checked, or a new tensor."""
+def _buffer(name, t, shape, dtype, like):
+    """``t``, checked, or a new tensor on the device of ``like``."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _check(name, t, dtype, dev)
-    if tuple(t.shape) != tuple(shape):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _check(name, t, dtype, like.get_device())
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 
 
-def _scratch(workspace, need, dev, what):
-    if need == 0:
-        raise MlaError(-2, what)
+def _scratch(workspace, need, like, what):
     if workspace is None:
-        return torch.zeros(need, dtype=torch.uint8, device=dev)
-    _check("workspace", workspace, torch.uint8, dev)
+        if need == 0:
+            raise MlaError(-2, what)
+        return torch.zeros(need, dtype=_U8, device=like.device)
+    _check("workspace", workspace, _U8, like.get_device())
     return workspace
 
 
 # ---------------------------------------------------------------- rotary positions and the cache write
 def _rope_append(name, q_pe, ckv, k_pe, positions, inv_freq, slots, cache, geometry, q_out, sections, interleaved,
                  stream):
-    dev = ckv.device
-    for n, t in (("ckv", ckv), ("k_pe", k_pe)):
-        _check(n, t, torch.bfloat16, dev, contiguous=False)
+    index = ckv.get_device()
+    _check("k_pe", k_pe, _BF16, index, False)
     tokens = ckv.shape[0]
     if ckv.shape != (tokens, HEAD_DIM_CKV) or k_pe.shape != (tokens, HEAD_DIM_KPE):
         raise ValueError("ckv must be [tokens, 512] and k_pe [tokens, 64]")
-    _check("positions", positions, torch.int32, dev)
-    if positions.dim() == 1:
-        positions = positions[None]
-    if positions.dim() != 2 or not 1 <= positions.shape[0] <= 3 or positions.shape[1] != tokens:
+    _check("positions", positions, _I32, index)
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dim() > 2 or not 1 <= axes <= 3 or positions.shape[-1] != tokens:
         raise ValueError("positions must be [tokens] or [axes, tokens] with one to three axes")
-    axes = positions.shape[0]
     if sections is None:
         if axes != 1:
             raise ValueError("sections (pairs of every axis) are needed with several axes")
         sections = (HEAD_DIM_KPE // 2,)
     if len(sections) != axes:
         raise ValueError("sections must name the pairs of every axis")
-    _check("inv_freq", inv_freq, torch.float32, dev)
+    _check("inv_freq", inv_freq, _F32, index)
     if inv_freq.shape != (HEAD_DIM_KPE // 2,):
         raise ValueError("inv_freq must be [32]")
-    _ints("slots", slots, (tokens,), dev)
-    heads, strides = 0, (0, 0)
+    _ints("slots", slots, (tokens,), index)
+    several = tokens > 1  # (the stride of a dimension of one element is never used)
+    heads = q_token = q_head = 0
     if q_pe is None:
         if q_out is not None:
             raise ValueError("q_out without q_pe")
     else:
-        _check("q_pe", q_pe, torch.bfloat16, dev, contiguous=False)
+        _check("q_pe", q_pe, _BF16, index, False)
         if q_pe.dim() != 3 or q_pe.shape[0] != tokens or q_pe.shape[2] != HEAD_DIM_KPE:
             raise ValueError("q_pe must be [tokens, H, 64]")
         heads = q_pe.shape[1]
-        # (the stride of a dimension of one element is never used)
-        strides = (q_pe.stride(0) if tokens > 1 else 0, q_pe.stride(1) if heads > 1 else 0)
-        q_out = _buffer("q_out", q_out, (tokens, heads, HEAD_DIM_KPE), torch.bfloat16, dev)
-    for n, t in (("q_pe", q_pe), ("ckv", ckv), ("k_pe", k_pe)):
-        if t is not None and t.numel() and t.stride(-1) != 1:
-            raise ValueError(f"the last dimension of {n} must be contiguous")
-    row = [t.stride(0) if tokens > 1 else 0 for t in (ckv, k_pe)]
-    dims = MlaRopeDims(tokens, heads, axes, (ctypes.c_int32 * 3)(*[int(x) for x in sections]), 1 if interleaved else 0,
-                       geometry[0], geometry[1], strides[0], strides[1], row[0], row[1])
-    _call(name, dev, stream, _at(q_pe), _at(ckv), _at(k_pe), _at(positions), _at(inv_freq), _at(slots), _at(q_out),
-          *[_at(c) for c in cache], ctypes.byref(dims))
+        q_token, q_head, last = q_pe.stride()
+        if last != 1 and tokens and heads:
+            raise ValueError("the last dimension of q_pe must be contiguous")
+        q_out = _buffer("q_out", q_out, (tokens, heads, HEAD_DIM_KPE), _BF16, q_pe)
+    ckv_row, ckv_last = ckv.stride()
+    kpe_row, kpe_last = k_pe.stride()
+    if (ckv_last != 1 or kpe_last != 1) and tokens:
+        raise ValueError("the last dimension of ckv and k_pe must be contiguous")
+    dims = MlaRopeDims(tokens, heads, axes, tuple(sections), 1 if interleaved else 0, geometry[0], geometry[1],
+                       q_token if several else 0, q_head if heads > 1 else 0, ckv_row if several else 0,
+                       kpe_row if several else 0)
+    _call(name, index, stream, _at(q_pe), ckv.data_ptr(), k_pe.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+          slots.data_ptr(), _at(q_out), *cache, ctypes.byref(dims))
     return q_out
 
 
@@ -142,40 +150,41 @@ def mla_rope_append(q_pe, ckv, k_pe, positions, inv_freq, slots, ckv_cache, kpe_
     the rotated keys to the bf16 cache's ``slots`` [tokens] (a slot outside the cache: not
     written).  inv_freq [32] float32.  The inputs may be slices of wider projections.
     Returns the rotated queries (q_out [tokens, H, 64]; None without q_pe)."""
-    geometry = _bf16_caches(ckv_cache, kpe_cache, ckv.device)
-    return _rope_append("mla_rope_append", q_pe, ckv, k_pe, positions, inv_freq, slots, (ckv_cache, kpe_cache),
-                        geometry, q_out, sections, interleaved, stream)
+    _check("ckv", ckv, _BF16, None, False)
+    geometry = _bf16_caches(ckv_cache, kpe_cache, ckv.get_device())
+    return _rope_append("mla_rope_append", q_pe, ckv, k_pe, positions, inv_freq, slots,
+                        (ckv_cache.data_ptr(), kpe_cache.data_ptr()), geometry, q_out, sections, interleaved, stream)
 
 
 def mla_rope_append_fp8(q_pe, ckv, k_pe, positions, inv_freq, slots, kv_fp8, q_out=None,
                         sections: Optional[Sequence[int]] = None, interleaved=True, stream=None):
     """``mla_rope_append`` into an FP8 cache: the latents are quantised in tiles of 128 (scale
     amax / 448, nearest E4M3), the rope part stays bf16."""
-    geometry = _fp8_cache(kv_fp8, ckv.device)
-    return _rope_append("mla_rope_append_fp8", q_pe, ckv, k_pe, positions, inv_freq, slots, (kv_fp8,), geometry, q_out,
-                        sections, interleaved, stream)
+    _check("ckv", ckv, _BF16, None, False)
+    geometry = _fp8_cache(kv_fp8, ckv.get_device())
+    return _rope_append("mla_rope_append_fp8", q_pe, ckv, k_pe, positions, inv_freq, slots, (kv_fp8.data_ptr(),), geometry,
+                        q_out, sections, interleaved, stream)
 
 
 # ---------------------------------------------------------------- tokens read back, page copies
-def _gather(name, cache, geometry, slots, ckv_out, kpe_out, count, stream):
-    dev = cache[0].device
-    _check("slots", slots, torch.int32, dev)
+def _count(count, index):
+    _check("count", count, _I32, index)
+    if count.numel() != 1:
+        raise ValueError("count must hold one int32")
+    return count.data_ptr()
+
+
+def _gather(name, cache, like, geometry, slots, ckv_out, kpe_out, count, stream):
+    index = like.get_device()
+    _check("slots", slots, _I32, index)
     if slots.dim() != 1:
         raise ValueError("slots must be [n]")
     n = slots.shape[0]
-    ckv_out = _buffer("ckv_out", ckv_out, (n, HEAD_DIM_CKV), torch.bfloat16, dev)
-    kpe_out = _buffer("kpe_out", kpe_out, (n, HEAD_DIM_KPE), torch.bfloat16, dev)
-    if count is not None:
-        _count(count, dev)
-    _call(name, dev, stream, *[_at(c) for c in cache], _at(slots), n, _at(count), geometry[0], geometry[1],
-          _at(ckv_out), _at(kpe_out))
+    ckv_out = _buffer("ckv_out", ckv_out, (n, HEAD_DIM_CKV), _BF16, like)
+    kpe_out = _buffer("kpe_out", kpe_out, (n, HEAD_DIM_KPE), _BF16, like)
+    _call(name, index, stream, *cache, slots.data_ptr(), n, None if count is None else _count(count, index),
+          geometry[0], geometry[1], ckv_out.data_ptr(), kpe_out.data_ptr())
     return ckv_out, kpe_out
-
-
-def _count(count, dev):
-    _check("count", count, torch.int32, dev)
-    if count.numel() != 1:
-        raise ValueError("count must hold one int32")
 
 
 def mla_cache_gather(ckv_cache, kpe_cache, slots, ckv_out=None, kpe_out=None, count=None,
@@ -184,27 +193,27 @@ def mla_cache_gather(ckv_cache, kpe_cache, slots, ckv_out=None, kpe_out=None, co
     for a slot outside the cache.  ``count`` (one int32 on the device): rows at or past it are
     left as they were."""
     geometry = _bf16_caches(ckv_cache, kpe_cache)
-    return _gather("mla_cache_gather", (ckv_cache, kpe_cache), geometry, slots, ckv_out, kpe_out, count, stream)
+    return _gather("mla_cache_gather", (ckv_cache.data_ptr(), kpe_cache.data_ptr()), ckv_cache, geometry, slots,
+                   ckv_out, kpe_out, count, stream)
 
 
 def mla_cache_gather_fp8(kv_fp8, slots, ckv_out=None, kpe_out=None, count=None,
                          stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """``mla_cache_gather`` from an FP8 cache: the bf16 values that the attention reads."""
-    return _gather("mla_cache_gather_fp8", (kv_fp8,), _fp8_cache(kv_fp8), slots, ckv_out, kpe_out, count, stream)
+    geometry = _fp8_cache(kv_fp8)
+    return _gather("mla_cache_gather_fp8", (kv_fp8.data_ptr(),), kv_fp8, geometry, slots, ckv_out, kpe_out, count,
+                   stream)
 
 
-def _copy_pages(name, cache, geometry, src, dst, tokens, count, stream):
-    dev = cache[0].device
-    _check("src", src, torch.int32, dev)
+def _copy_pages(name, cache, index, geometry, src, dst, tokens, count, stream):
+    _check("src", src, _I32, index)
     if src.dim() != 1:
         raise ValueError("src must be [n]")
-    _ints("dst", dst, src.shape, dev)
+    _ints("dst", dst, src.shape, index)
     if tokens is not None:
-        _ints("tokens", tokens, src.shape, dev)
-    if count is not None:
-        _count(count, dev)
-    _call(name, dev, stream, *[_at(c) for c in cache], _at(src), _at(dst), _at(tokens), src.shape[0], _at(count),
-          geometry[0], geometry[1])
+        _ints("tokens", tokens, src.shape, index)
+    _call(name, index, stream, *cache, src.data_ptr(), dst.data_ptr(), _at(tokens), src.shape[0],
+          None if count is None else _count(count, index), geometry[0], geometry[1])
 
 
 def mla_cache_copy_pages(ckv_cache, kpe_cache, src, dst, tokens=None, count=None, stream=None) -> None:
@@ -212,12 +221,15 @@ def mla_cache_copy_pages(ckv_cache, kpe_cache, src, dst, tokens=None, count=None
     entries with a page outside the cache copy nothing.  ``count`` (one int32 on the device):
     entries at or past it are not read."""
     geometry = _bf16_caches(ckv_cache, kpe_cache)
-    _copy_pages("mla_cache_copy_pages", (ckv_cache, kpe_cache), geometry, src, dst, tokens, count, stream)
+    _copy_pages("mla_cache_copy_pages", (ckv_cache.data_ptr(), kpe_cache.data_ptr()), ckv_cache.get_device(), geometry,
+                src, dst, tokens, count, stream)
 
 
 def mla_cache_copy_pages_fp8(kv_fp8, src, dst, tokens=None, count=None, stream=None) -> None:
     """``mla_cache_copy_pages`` for an FP8 cache."""
-    _copy_pages("mla_cache_copy_pages_fp8", (kv_fp8,), _fp8_cache(kv_fp8), src, dst, tokens, count, stream)
+    geometry = _fp8_cache(kv_fp8)
+    _copy_pages("mla_cache_copy_pages_fp8", (kv_fp8.data_ptr(),), kv_fp8.get_device(), geometry, src, dst, tokens,
+                count, stream)
 
 
 # ---------------------------------------------------------------- the FP8 chunk prefill
@@ -231,29 +243,33 @@ def mla_paged_prefill_fp8(q_nope, q_pe, kv_fp8, qo_indptr, kv_indptr, kv_indices
     """Causal attention (bottom-right aligned) of a chunk of new tokens over an FP8 cache:
     ``mla_paged_prefill`` with kv_fp8 [num_pages, page_size, 656].  Returns (out, lse); rows
     behind qo_indptr's last request are left as they were."""
-    dev = q_nope.device
-    for n, t in (("q_nope", q_nope), ("q_pe", q_pe)):
-        _check(n, t, torch.bfloat16, dev)
+    _check("q_nope", q_nope, _BF16)
+    index = q_nope.get_device()
+    _check("q_pe", q_pe, _BF16, index)
     if q_nope.dim() != 3:
         raise ValueError("q_nope must be [total_q, H, 512]")
     rows, heads = q_nope.shape[0], q_nope.shape[1]
     if q_nope.shape != (rows, heads, HEAD_DIM_CKV) or q_pe.shape != (rows, heads, HEAD_DIM_KPE):
         raise ValueError("q_nope must be [total_q, H, 512] and q_pe [total_q, H, 64]")
-    num_pages, page_size = _fp8_cache(kv_fp8, dev)
-    for n, t in (("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr), ("kv_indices", kv_indices)):
-        _check(n, t, torch.int32, dev)
+    num_pages, page_size = _fp8_cache(kv_fp8, index)
+    _check("qo_indptr", qo_indptr, _I32, index)
+    _check("kv_indptr", kv_indptr, _I32, index)
+    _check("kv_indices", kv_indices, _I32, index)
     batch = kv_indptr.numel() - 1
     if batch < 0 or qo_indptr.numel() != batch + 1:
         raise ValueError("qo_indptr and kv_indptr must both have batch + 1 entries")
     dims = make_dims(batch, heads, num_pages, page_size, kv_indices.numel(), total_q=rows, num_workers=num_workers)
-    out = _buffer("out", out, (rows, heads, HEAD_DIM_CKV), torch.bfloat16, dev)
-    lse = _buffer("lse", lse, (rows, heads), torch.float32, dev)
-    with torch.cuda.device(dev):
-        need = workspace_bytes_prefill_fp8(dims)
-    workspace = _scratch(workspace, need, dev, "mla_workspace_bytes_prefill_fp8")
-    _call("mla_paged_prefill_fp8", dev, stream, _at(q_nope), _at(q_pe), _at(kv_fp8), _at(qo_indptr), _at(kv_indptr),
-          _at(kv_indices), float(sm_scale), _at(out), _at(lse), ctypes.byref(dims), _at(workspace), workspace.numel(),
-          int(flags))
+    out = _buffer("out", out, (rows, heads, HEAD_DIM_CKV), _BF16, q_nope)
+    lse = _buffer("lse", lse, (rows, heads), _F32, q_nope)
+    if workspace is None:
+        with torch.cuda.device(index):
+            need = workspace_bytes_prefill_fp8(dims)
+        workspace = _scratch(None, need, q_nope, "mla_workspace_bytes_prefill_fp8")
+    else:  # (the library checks its size)
+        _check("workspace", workspace, _U8, index)
+    _call("mla_paged_prefill_fp8", index, stream, q_nope.data_ptr(), q_pe.data_ptr(), kv_fp8.data_ptr(),
+          qo_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), sm_scale, out.data_ptr(), lse.data_ptr(),
+          ctypes.byref(dims), workspace.data_ptr(), workspace.numel(), flags)
     return out, lse
 
 
@@ -264,23 +280,33 @@ def workspace_bytes_pages(max_rows: int, num_pages: int, entries: int) -> int:
     return int(lib().mla_workspace_bytes_pages(ctypes.byref(pool), int(entries)))
 
 
-def _pool(block_table, seq_lens, ref_count, page_size) -> MlaPool:
-    _check("block_table", block_table, torch.int32)
+def _pool(block_table, seq_lens, ref_count, page_size):
+    """The pool's description and device."""
+    _check("block_table", block_table, _I32)
+    index = block_table.get_device()
     if block_table.dim() != 2:
         raise ValueError("block_table must be [max_rows, max_blocks]")
-    _ints("seq_lens", seq_lens, block_table.shape[:1], block_table.device)
-    _check("ref_count", ref_count, torch.int32, block_table.device)
+    rows, blocks = block_table.shape
+    _ints("seq_lens", seq_lens, (rows,), index)
+    _check("ref_count", ref_count, _I32, index)
     if ref_count.dim() != 1:
         raise ValueError("ref_count must be [num_pages]")
-    return MlaPool(block_table.data_ptr(), seq_lens.data_ptr(), ref_count.data_ptr(), block_table.shape[0],
-                   block_table.shape[1], ref_count.shape[0], int(page_size))
+    return MlaPool(block_table.data_ptr(), seq_lens.data_ptr(), ref_count.data_ptr(), rows, blocks, ref_count.shape[0],
+                   page_size), index
 
 
-def _pool_scratch(workspace, pool, n, dev):
+def _entries(name, t, index):
+    _check(name, t, _I32, index)
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be [n]")
+    return t.shape[0]
+
+
+def _pool_scratch(workspace, pool, n, like):
     if workspace is not None:  # (the library checks its size)
-        _check("workspace", workspace, torch.uint8, dev)
+        _check("workspace", workspace, _U8, like.get_device())
         return workspace
-    return _scratch(None, int(lib().mla_workspace_bytes_pages(ctypes.byref(pool), n)), dev,
+    return _scratch(None, int(lib().mla_workspace_bytes_pages(ctypes.byref(pool), n)), like,
                     "mla_workspace_bytes_pages")
 
 
@@ -290,21 +316,19 @@ def mla_pages_extend(block_table, seq_lens, ref_count, rows, new_tokens, page_si
     [capacity], results [n]): where the granted tokens of every entry are in ``slots``, their
     token slots (-1 past the last), and 0 or the status of a refused entry (-6 bad index,
     -11 too few free pages)."""
-    dev = block_table.device
-    pool = _pool(block_table, seq_lens, ref_count, page_size)
-    _check("rows", rows, torch.int32, dev)
-    n = rows.numel()
-    _ints("rows", rows, (n,), dev)
-    _ints("new_tokens", new_tokens, (n,), dev)
+    pool, index = _pool(block_table, seq_lens, ref_count, page_size)
+    n = _entries("rows", rows, index)
+    _ints("new_tokens", new_tokens, (n,), index)
     capacity = int(capacity)
     if capacity < 0:
         raise ValueError("capacity must not be negative")
-    new_indptr = _buffer("new_indptr", new_indptr, (n + 1,), torch.int32, dev)
-    slots = _buffer("slots", slots, (capacity,), torch.int32, dev)
-    results = _buffer("results", results, (n,), torch.int32, dev)
-    workspace = _pool_scratch(workspace, pool, n, dev)
-    _call("mla_pages_extend", dev, stream, ctypes.byref(pool), _at(rows), _at(new_tokens), n, _at(new_indptr),
-          _at(slots), capacity, _at(results), _at(workspace), workspace.numel())
+    new_indptr = _buffer("new_indptr", new_indptr, (n + 1,), _I32, block_table)
+    slots = _buffer("slots", slots, (capacity,), _I32, block_table)
+    results = _buffer("results", results, (n,), _I32, block_table)
+    workspace = _pool_scratch(workspace, pool, n, block_table)
+    _call("mla_pages_extend", index, stream, ctypes.byref(pool), rows.data_ptr(), new_tokens.data_ptr(), n,
+          new_indptr.data_ptr(), slots.data_ptr(), capacity, results.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
     return new_indptr, slots, results
 
 
@@ -313,28 +337,25 @@ def mla_pages_fork(block_table, seq_lens, ref_count, parents, children, page_siz
     """Row children[i] (empty) becomes a copy of row parents[i]; full pages are shared.
     Returns (results, src, dst, copy_tokens) [n]: the partly filled pages to copy with
     ``mla_cache_copy_pages(..., src, dst, tokens=copy_tokens)`` for every cache."""
-    dev = block_table.device
-    pool = _pool(block_table, seq_lens, ref_count, page_size)
-    _check("parents", parents, torch.int32, dev)
-    n = parents.numel()
-    _ints("parents", parents, (n,), dev)
-    _ints("children", children, (n,), dev)
-    results = _buffer("results", results, (n,), torch.int32, dev)
-    src = _buffer("src", src, (n,), torch.int32, dev)
-    dst = _buffer("dst", dst, (n,), torch.int32, dev)
-    copy_tokens = _buffer("copy_tokens", copy_tokens, (n,), torch.int32, dev)
-    workspace = _pool_scratch(workspace, pool, n, dev)
-    _call("mla_pages_fork", dev, stream, ctypes.byref(pool), _at(parents), _at(children), n, _at(src), _at(dst),
-          _at(copy_tokens), _at(results), _at(workspace), workspace.numel())
+    pool, index = _pool(block_table, seq_lens, ref_count, page_size)
+    n = _entries("parents", parents, index)
+    _ints("children", children, (n,), index)
+    results = _buffer("results", results, (n,), _I32, block_table)
+    src = _buffer("src", src, (n,), _I32, block_table)
+    dst = _buffer("dst", dst, (n,), _I32, block_table)
+    copy_tokens = _buffer("copy_tokens", copy_tokens, (n,), _I32, block_table)
+    workspace = _pool_scratch(workspace, pool, n, block_table)
+    _call("mla_pages_fork", index, stream, ctypes.byref(pool), parents.data_ptr(), children.data_ptr(), n,
+          src.data_ptr(), dst.data_ptr(), copy_tokens.data_ptr(), results.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
     return results, src, dst, copy_tokens
 
 
 def mla_pages_free(block_table, seq_lens, ref_count, rows, page_size, stream=None) -> None:
     """The listed rows give up their pages and are empty."""
-    dev = block_table.device
-    pool = _pool(block_table, seq_lens, ref_count, page_size)
-    _check("rows", rows, torch.int32, dev)
-    _call("mla_pages_free", dev, stream, ctypes.byref(pool), _at(rows), rows.numel())
+    pool, index = _pool(block_table, seq_lens, ref_count, page_size)
+    n = _entries("rows", rows, index)
+    _call("mla_pages_free", index, stream, ctypes.byref(pool), rows.data_ptr(), n)
 
 
 def mla_pages_compact(block_table, seq_lens, ref_count, page_size, counts=None, src=None, dst=None, workspace=None,
@@ -342,13 +363,12 @@ def mla_pages_compact(block_table, seq_lens, ref_count, page_size, counts=None, 
     """Move the live pages to the front.  Returns (counts [2]: live pages and moves, src, dst
     [num_pages // 2]): the moves, to be copied with ``mla_cache_copy_pages(..., src, dst,
     count=counts[1:])`` for every cache."""
-    dev = block_table.device
-    pool = _pool(block_table, seq_lens, ref_count, page_size)
+    pool, index = _pool(block_table, seq_lens, ref_count, page_size)
     moves = ref_count.shape[0] // 2
-    counts = _buffer("counts", counts, (2,), torch.int32, dev)
-    src = _buffer("src", src, (moves,), torch.int32, dev)
-    dst = _buffer("dst", dst, (moves,), torch.int32, dev)
-    workspace = _pool_scratch(workspace, pool, 0, dev)
-    _call("mla_pages_compact", dev, stream, ctypes.byref(pool), _at(counts), _at(src), _at(dst), _at(workspace),
-          workspace.numel())
+    counts = _buffer("counts", counts, (2,), _I32, block_table)
+    src = _buffer("src", src, (moves,), _I32, block_table)
+    dst = _buffer("dst", dst, (moves,), _I32, block_table)
+    workspace = _pool_scratch(workspace, pool, 0, block_table)
+    _call("mla_pages_compact", index, stream, ctypes.byref(pool), counts.data_ptr(), src.data_ptr(), dst.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return counts, src, dst

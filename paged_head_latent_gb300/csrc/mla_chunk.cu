@@ -192,6 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan and the staged keys
   // All 512 columns are ours, so they start at 0, and the products' addresses are constants.
   const uint32_t tmem = 0;
   if (misc.tmem != 0 && threadIdx.x == 0) {
@@ -559,8 +560,19 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, cudaStream
       configured[dev] = true;
     }
   }
-  chunk_kernel<<<2 * p.workers, kThreads, kSmem, stream>>>(maps, p);
-  return cudaGetLastError();
+  // A programmatic dependent of the staging pass: this kernel's start overlaps that one's tail.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.workers);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel, maps, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace mla

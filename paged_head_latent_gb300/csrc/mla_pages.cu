@@ -7,10 +7,12 @@
 // outcome is unique whatever the order of the kernels' threads, and the pages it fills lie
 // at the front of the cache.
 //
-// A call is a few launches on one stream: a bitmap of the free pages (one pass over
-// ref_count, 4 bytes a page), one block that numbers them and decides every entry, and a
-// grid that applies the decisions.  Nothing but integers is computed; the counters that
-// several threads change are changed by integer atomics, whose order does not matter.
+// A call is two launches on one stream: one block that makes a bitmap of the free pages (one
+// pass over ref_count, 4 bytes a page), numbers them and decides every entry, and a grid that
+// applies the decisions.  For a pool of more than 65,536 pages a grid makes the bitmap first.
+// Nothing but integers is computed; the counters that several threads change are changed by
+// integer atomics, whose order does not matter.  What bounds these calls is latency: the
+// plan is a chain of dependent loads (row, length, last page, its count) and block scans.
 #include "launch.h"
 #include "mla_paged.h"
 
@@ -69,36 +71,70 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part, lo
   return before + incl - v;
 }
 
-// Free pages before every word; returns the number of free pages.
-__device__ __forceinline__ long long number_free(const PoolParams& p, const PoolWork& w, long long* part) {
-  const int words = (p.num_pages + 31) / 32;
-  long long run = 0, total;
-  for (int base = 0; base < words; base += kPlanThreads) {
-    const int i = base + threadIdx.x;
-    const long long c = i < words ? __popc(w.bits[i]) : 0;
-    const long long at = run + block_scan(c, part, &total);
-    if (i < words) w.before[i] = (int32_t)at;
-    run += total;
-  }
-  return run;
-}
+// The free pages of a pool, as the plan's block sees them.  kNear: the block makes the bitmap
+// itself and keeps it in shared memory (with the pages before every word); otherwise both
+// are in the workspace.
+template <bool kNear>
+struct FreePages {
+  const PoolParams& p;
+  const PoolWork& w;
+  uint32_t* bits;
+  int32_t* before;
+  __device__ FreePages(const PoolParams& pool, const PoolWork& work, uint32_t* near_bits, int32_t* near_before)
+      : p(pool), w(work), bits(kNear ? near_bits : work.bits), before(kNear ? near_before : work.before) {}
 
-// The ids of the first `need` free pages, in order.
-__device__ __forceinline__ void list_free(const PoolParams& p, const PoolWork& w, long long need) {
-  const int words = (p.num_pages + 31) / 32;
-  for (int i = threadIdx.x; i < words; i += kPlanThreads) {
-    uint32_t b = w.bits[i];
-    for (long long r = w.before[i]; b && r < need; ++r, b &= b - 1) w.pages[r] = 32 * i + __ffs(b) - 1;
+  // Numbers the free pages and returns how many there are (called by the whole block).
+  __device__ long long number(long long* part) {
+    const int words = (p.num_pages + 31) / 32;
+    if constexpr (kNear) {
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      for (int w0 = 8 * warp; w0 < words; w0 += 8 * (kPlanThreads / 32)) {  // eight words of a warp in flight
+        int32_t ref[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int page = 32 * (w0 + k) + lane;
+          ref[k] = page < p.num_pages ? p.ref_count[page] : 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const unsigned b = __ballot_sync(0xffffffffu, ref[k] <= 0);
+          if (lane == 0 && w0 + k < words) bits[w0 + k] = b;
+        }
+      }
+      __syncthreads();
+    }
+    long long run = 0, total;
+    for (int base = 0; base < words; base += kPlanThreads) {
+      const int i = base + threadIdx.x;
+      const long long c = i < words ? __popc(bits[i]) : 0;
+      const long long at = run + block_scan(c, part, &total);
+      if (i < words) before[i] = (int32_t)at;
+      run += total;
+    }
+    return run;
   }
-}
+
+  // The ids of the first `need` free pages, in order.
+  __device__ void list(long long need) {
+    const int words = (p.num_pages + 31) / 32;
+    for (int i = threadIdx.x; i < words; i += kPlanThreads) {
+      uint32_t b = bits[i];
+      for (long long r = before[i]; b && r < need; ++r, b &= b - 1) w.pages[r] = 32 * i + __ffs(b) - 1;
+    }
+  }
+};
+
+constexpr int kNearWords = 2048;  // 65,536 pages: the plan's block reads their counts in about 2 us
 
 // One block: decides every entry in list order.  Entry i is valid if its indices are and no
 // earlier entry names its row; a valid entry is granted if it needs no page, or if the
 // pages that the valid entries up to and including it need are there.
-template <bool kFork>
+template <bool kFork, bool kNear>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolParams p, PoolWork w) {
   __shared__ long long part[32];
-  const long long free_pages = number_free(p, w, part);
+  __shared__ uint32_t near_bits[kNear ? kNearWords : 1];
+  __shared__ int32_t near_before[kNear ? kNearWords : 1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int32_t* rows = kFork ? p.children : p.rows;
   auto good_row = [&](int r) { return r >= 0 && r < p.max_rows; };
   for (int i = threadIdx.x; i < p.n; i += kPlanThreads)
@@ -106,6 +142,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolParams p, PoolWo
   __syncthreads();
   for (int i = threadIdx.x; i < p.n; i += kPlanThreads)
     if (good_row(rows[i])) atomicMin(&w.claim[rows[i]], i);
+  FreePages<kNear> free(p, w, near_bits, near_before);
+  const long long free_pages = free.number(part);
   __syncthreads();
   const long long room = (long long)p.max_blocks * p.page_size;
   long long need_run = 0, new_run = 0, taken = 0, total;
@@ -113,7 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolParams p, PoolWo
     const int i = base + threadIdx.x;
     bool ok = false;
     int len = 0, add = 0, need = 0;
-    if (i < p.n && good_row(rows[i]) && w.claim[rows[i]] == i) {
+    if (i < p.n && good_row(rows[i]) && __ldcg(&w.claim[rows[i]]) == i) {
       const int row = rows[i];
       if constexpr (kFork) {
         const int parent = p.parents[i];
@@ -154,11 +192,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolParams p, PoolWo
     }
   }
   if (!kFork && threadIdx.x == 0) p.new_indptr[p.n] = (int32_t)new_run;
-  list_free(p, w, taken);
+  free.list(taken);
 }
 
 // One block per entry: the row's new blocks, their counts, and the new tokens' slots.
 __global__ void __launch_bounds__(kApplyThreads) extend_kernel(PoolParams p, PoolWork w) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
     const int len = w.old_len[i];
     if (len < 0) continue;
@@ -188,6 +227,7 @@ __global__ void __launch_bounds__(kApplyThreads) extend_kernel(PoolParams p, Poo
 
 // One block per pair: the parent's full pages are shared, its partial page is listed for copying.
 __global__ void __launch_bounds__(kApplyThreads) fork_kernel(PoolParams p, PoolWork w) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
     const int len = w.old_len[i];
     int src = -1, dst = -1, tokens = 0;
@@ -245,41 +285,65 @@ __device__ __forceinline__ int free_before(const PoolWork& w, int page) {
   return w.before[page >> 5] + __popc(w.bits[page >> 5] & ((1u << (page & 31)) - 1u));
 }
 
-__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PoolParams p, PoolWork w) {
-  __shared__ long long part[32];
-  const int live = p.num_pages - (int)number_free(p, w, part);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    p.counts[0] = live;
-    p.counts[1] = live < p.num_pages ? free_before(w, live) : 0;  // no page is free: none moves
+// The j-th free page (j < the number of free pages).
+__device__ __forceinline__ int free_page(const PoolWork& w, int words, int j) {
+  int lo = 0, hi = words - 1;  // last word with at most j free pages before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (w.before[mid] <= j) lo = mid; else hi = mid - 1;
   }
+  uint32_t b = w.bits[lo];
+  for (int k = j - w.before[lo]; k > 0; --k) b &= b - 1;
+  return 32 * lo + __ffs(b) - 1;
 }
 
-__global__ void __launch_bounds__(256) compact_list_kernel(PoolParams p, PoolWork w) {
-  const int live = p.counts[0], moves = p.counts[1];
-  const int tid = blockIdx.x * blockDim.x + threadIdx.x, step = gridDim.x * blockDim.x;
-  for (int page = tid; page < p.num_pages; page += step) {
-    const bool is_free = (w.bits[page >> 5] >> (page & 31)) & 1u;
-    if (page < live && is_free) p.dst[free_before(w, page)] = page;
-    if (page >= live && !is_free) p.src[page - free_before(w, page) - (live - moves)] = page;
+template <bool kNear>
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PoolParams p, PoolWork w) {
+  __shared__ long long part[32];
+  __shared__ uint32_t near_bits[kNear ? kNearWords : 1];
+  __shared__ int32_t near_before[kNear ? kNearWords : 1];
+  __shared__ int moves;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  FreePages<kNear> free(p, w, near_bits, near_before);
+  const int live = p.num_pages - (int)free.number(part);
+  if (threadIdx.x == 0) moves = 0;  // (no page is free: none moves)
+  __syncthreads();
+  const int words = (p.num_pages + 31) / 32;
+  if constexpr (kNear)
+    for (int i = threadIdx.x; i < words; i += kPlanThreads) {
+      w.bits[i] = free.bits[i];
+      w.before[i] = free.before[i];
+    }
+  if (threadIdx.x == 0) {
+    if (live < p.num_pages)
+      moves = free.before[live >> 5] + __popc(free.bits[live >> 5] & ((1u << (live & 31)) - 1u));
+    p.counts[0] = live;
+    p.counts[1] = moves;
   }
-  for (int k = moves + tid; k < p.num_pages / 2; k += step) p.src[k] = p.dst[k] = -1;
 }
 
 __global__ void __launch_bounds__(256) compact_apply_kernel(PoolParams p, PoolWork w) {
-  const int live = p.counts[0], moves = p.counts[1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int live = p.counts[0], moves = p.counts[1], words = (p.num_pages + 31) / 32;
   const long long tid = blockIdx.x * blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
-  for (long long k = tid; k < moves; k += step) {
-    p.ref_count[p.dst[k]] = p.ref_count[p.src[k]];
-    p.ref_count[p.src[k]] = 0;
+  auto is_free = [&](int page) { return (w.bits[page >> 5] >> (page & 31)) & 1u; };
+  auto move_of = [&](int page) { return page - free_before(w, page) - (live - moves); };  // of a live page >= live
+  for (long long page = live + tid; page < p.num_pages; page += step) {
+    if (is_free((int)page)) continue;
+    const int j = move_of((int)page), to = free_page(w, words, j);
+    p.src[j] = (int)page;
+    p.dst[j] = to;
+    p.ref_count[to] = p.ref_count[page];
+    p.ref_count[page] = 0;
   }
+  for (long long k = moves + tid; k < p.num_pages / 2; k += step) p.src[k] = p.dst[k] = -1;
   const long long cells = (long long)p.max_rows * p.max_blocks;
   for (long long c = tid; c < cells; c += step) {
     const int row = (int)(c / p.max_blocks), k = (int)(c - (long long)row * p.max_blocks);
     if (k >= blocks_of(p.seq_lens[row], p.page_size)) continue;
     const int page = p.block_table[c];
-    if (page < live || page >= p.num_pages || ((w.bits[page >> 5] >> (page & 31)) & 1u)) continue;
-    p.block_table[c] = p.dst[page - free_before(w, page) - (live - moves)];
+    if (page < live || page >= p.num_pages || is_free(page)) continue;
+    p.block_table[c] = free_page(w, words, move_of(page));
   }
 }
 
@@ -288,29 +352,50 @@ int grid_of(long long threads, int block, int most) {
   return (int)(g < 1 ? 1 : g > most ? most : g);
 }
 
+bool near_pool(const PoolParams& p) { return p.num_pages <= 32 * kNearWords; }
+
+// The bitmap of a large pool.
 cudaError_t launch_bitmap(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
+  if (near_pool(p)) return cudaSuccess;
   free_bitmap_kernel<<<grid_of(p.num_pages, 256, 1216), 256, 0, stream>>>(p, w.bits);
+  return cudaGetLastError();
+}
+
+// A programmatic dependent of the plan: its launch overlaps the plan.
+template <typename K>
+cudaError_t launch_apply(K kernel, int grid, int threads, const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, w);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool kFork>
+cudaError_t launch_plan(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
+  const cudaError_t e = launch_bitmap(p, w, stream);
+  if (e != cudaSuccess) return e;
+  if (near_pool(p)) plan_kernel<kFork, true><<<1, kPlanThreads, 0, stream>>>(p, w);
+  else plan_kernel<kFork, false><<<1, kPlanThreads, 0, stream>>>(p, w);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_pages_extend(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
-  cudaError_t e = launch_bitmap(p, w, stream);
-  if (e != cudaSuccess) return e;
-  plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(p, w);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  extend_kernel<<<p.n < 1 ? 1 : p.n < 4096 ? p.n : 4096, kApplyThreads, 0, stream>>>(p, w);
-  return cudaGetLastError();
+  const cudaError_t e = launch_plan<false>(p, w, stream);
+  return e != cudaSuccess ? e : launch_apply(extend_kernel, p.n < 1 ? 1 : p.n < 4096 ? p.n : 4096, kApplyThreads, p, w, stream);
 }
 
 cudaError_t launch_pages_fork(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
-  cudaError_t e = launch_bitmap(p, w, stream);
-  if (e != cudaSuccess) return e;
-  plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(p, w);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  fork_kernel<<<p.n < 4096 ? p.n : 4096, kApplyThreads, 0, stream>>>(p, w);
-  return cudaGetLastError();
+  const cudaError_t e = launch_plan<true>(p, w, stream);
+  return e != cudaSuccess ? e : launch_apply(fork_kernel, p.n < 4096 ? p.n : 4096, kApplyThreads, p, w, stream);
 }
 
 cudaError_t launch_pages_free(const PoolParams& p, cudaStream_t stream) {
@@ -321,12 +406,11 @@ cudaError_t launch_pages_free(const PoolParams& p, cudaStream_t stream) {
 cudaError_t launch_pages_compact(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
   cudaError_t e = launch_bitmap(p, w, stream);
   if (e != cudaSuccess) return e;
-  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, w);
+  if (near_pool(p)) compact_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(p, w);
+  else compact_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(p, w);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  compact_list_kernel<<<grid_of(p.num_pages, 256, 1216), 256, 0, stream>>>(p, w);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  compact_apply_kernel<<<grid_of((long long)p.max_rows * p.max_blocks, 256, 1216), 256, 0, stream>>>(p, w);
-  return cudaGetLastError();
+  const long long threads = (long long)p.max_rows * p.max_blocks > p.num_pages ? (long long)p.max_rows * p.max_blocks : p.num_pages;
+  return launch_apply(compact_apply_kernel, grid_of(threads, 256, 1216), 256, p, w, stream);
 }
 
 }  // namespace mla

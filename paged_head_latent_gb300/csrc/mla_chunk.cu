@@ -31,7 +31,6 @@
 // the output's columns), 8 loads Q and K, 9 loads V, 10 issues the products (leader SM only), 11
 // tensor memory.
 #include <mutex>
-#include <type_traits>
 
 #include "chunk.h"
 #include "ptx.cuh"
@@ -88,14 +87,18 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void mma2(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+// The operands' descriptors are given by their low words (address and leading offset): the
+// high word (stride 1024, 128-byte swizzle) is the same for all.
+__device__ __forceinline__ void mma2(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                      uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %6};\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(issue)
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(issue), "n"((1024 >> 4) | (1 << 14) | (2 << 29))
       : "memory");
 }
 // Arrive on the barrier at this offset in both SMs when the products issued so far are done.
@@ -249,33 +252,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products (leader SM)
-    // The whole warp runs this, with one elected thread issuing, and the operands are constants
-    // plus warp-uniform values: an issue then costs less than its product (32 cycles for S, 64
-    // for O).  From a single thread of a divergent warp every issue took 66 cycles, from
-    // operands computed at run time 145.  A failed wait does not branch before the tile's end.
+    // The whole warp runs this, with one elected thread issuing, and the loop is short enough
+    // straight-line code with operands that are constants plus warp-uniform values, so that an
+    // issue costs less than its product (32 cycles for S, 64 for O).  Measured on four prompts
+    // with 128 heads: from one thread of a divergent warp 1299 us, with 64-bit descriptors and
+    // a copy of S's products for each buffer 1114, as it is 907, with the loops rolled 1012-1324.
+    // A failed wait does not branch before the tile's end.
     if (rank == 0 && sound) {
       constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256, false, true);
-      const uint64_t q0 = smem_desc_sw128(base + kOffQ, 16, 1024), k0 = smem_desc_sw128(base + kOffK, 16, 1024);
-      const uint64_t p0 = smem_desc_sw128(base + kOffP, 16, 1024), v0 = smem_desc_sw128(base + kOffV, kBox, 1024);
+      auto low = [&](uint32_t off, uint32_t lead) { return ((base + off) >> 4) | (lead >> 4) << 16; };
+      const uint32_t q0 = low(kOffQ, 16), k0 = low(kOffK, 16), p0 = low(kOffP, 16), v0 = low(kOffV, kBox);
       const uint32_t issue = elect_one();
       bool good = true;
       auto wait = [&](uint32_t i, uint32_t parity) {
         good &= mbar_wait(bar(i), parity, abort, p.status, kStatusTimeout, p.wait_ns);
         __syncwarp();
+        tc_fence_after();
       };
-      auto scores = [&](uint32_t j, auto buffer) {  // S of tile j
+      auto scores = [&](uint32_t j) {  // S of tile j
+        const uint32_t dst = kColS + 64 * (j & 1);
 #pragma unroll
         for (uint32_t g = 0; g < kKGroups; ++g) {
           wait(K_FULL + g, j & 1);
-          tc_fence_after();
 #pragma unroll
           for (uint32_t c = kGroup * g; c < kGroup * (g + 1); ++c)
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
-              mma2(issue, kColS + 64 * decltype(buffer)::value, q0 + c * (kBox / 16) + 2 * k, k0 + c * (kBox / 16) + 2 * k,
-                   kIdescS, c + k > 0);
-          commit2(issue, bar(g < kKGroups - 1 ? K_EMPTY + g : S_FULL + decltype(buffer)::value));
+              mma2(issue, dst, q0 + c * (kBox / 16) + 2 * k, k0 + c * (kBox / 16) + 2 * k, kIdescS, c + k > 0);
+          commit2(issue, bar(g < kKGroups - 1 ? K_EMPTY + g : S_FULL + (j & 1)));
         }
       };
       auto output = [&](uint32_t j, bool first, uint32_t seg) {  // O += P V of tile j
@@ -284,7 +289,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
           wait(V_FULL + h, j & 1);
-          tc_fence_after();
 #pragma unroll
           for (uint32_t n = 0; n < 2; ++n)
 #pragma unroll
@@ -301,10 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t n = it.t_end - it.t;
         wait(Q_FULL, it.seg & 1);
         for (uint32_t i = 0; i <= n; ++i) {
-          if (i < n) {
-            if ((j + i) & 1) scores(j + i, std::integral_constant<uint32_t, 1>{});
-            else scores(j + i, std::integral_constant<uint32_t, 0>{});
-          }
+          if (i < n) scores(j + i);
           if (i > 0) output(j + i - 1, i == 1, it.seg);
           if (!__all_sync(0xffffffffu, good)) break;
         }

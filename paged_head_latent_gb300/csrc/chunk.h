@@ -21,9 +21,17 @@ struct ChunkBlock {
   long long cost0;  // cost units before this block
 };
 
-// Where a worker's range starts: tile t of block i.
+// Where a worker's range starts: tile t of block i (a copy of which saves a load's latency).
 struct ChunkStart {
   int i, t;
+  ChunkBlock blk;
+};
+
+// A split block that a worker holds the last tile of: its rows, the worker that holds its
+// first tile (fragment slot 0 or 1 there, 0 everywhere else).
+struct ChunkMerge {
+  int row0, rows;  // rows = 0: none
+  int first, slot;
 };
 
 struct ChunkParams {
@@ -39,6 +47,7 @@ struct ChunkParams {
   // workspace
   uint32_t* status;
   ChunkStart* starts;   // [workers + 1]
+  ChunkMerge* merges;   // [workers]
   int32_t* first_block; // [batch + 1]
   ChunkBlock* blocks;
   uint32_t* flags;      // [tiles][8]: 128 bits "is a key", 128 bits "holds a value that is not finite"
@@ -57,13 +66,14 @@ struct ChunkMaps {
 };
 
 struct ChunkLayout {
-  size_t starts, first_block, blocks, flags, part_lse, part_o, ckv, kpe, total;
+  size_t starts, merges, first_block, blocks, flags, part_lse, part_o, ckv, kpe, total;
   long long tiles, max_blocks;
   ChunkLayout(int workers, int heads, int batch, int total_q, int num_kv_indices) {
     tiles = ((long long)num_kv_indices + kChunkKeys - 1) / kChunkKeys + batch;
     max_blocks = ((long long)total_q * heads + kChunkRows - 1) / kChunkRows + batch;
     starts = 256;
-    first_block = align_up(starts + ((size_t)workers + 1) * sizeof(ChunkStart), 256);
+    merges = align_up(starts + ((size_t)workers + 1) * sizeof(ChunkStart), 256);
+    first_block = align_up(merges + (size_t)workers * sizeof(ChunkMerge), 256);
     blocks = align_up(first_block + ((size_t)batch + 1) * sizeof(int32_t), 256);
     flags = align_up(blocks + (size_t)max_blocks * sizeof(ChunkBlock), 256);
     part_lse = align_up(flags + (size_t)tiles * 32, 256);

@@ -455,6 +455,7 @@ int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_f
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.starts = reinterpret_cast<mla::ChunkStart*>(ws + lay.starts);
+  p.merges = reinterpret_cast<mla::ChunkMerge*>(ws + lay.merges);
   p.first_block = reinterpret_cast<int32_t*>(ws + lay.first_block);
   p.blocks = reinterpret_cast<mla::ChunkBlock*>(ws + lay.blocks);
   p.flags = reinterpret_cast<uint32_t*>(ws + lay.flags);

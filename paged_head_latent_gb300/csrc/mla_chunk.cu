@@ -137,30 +137,32 @@ __device__ __forceinline__ void rows_release(int warp) {
 // A worker's tiles in order, segment by segment (a segment: tiles of one block).
 struct Walk {
   const ChunkParams& p;
-  ChunkStart at, end;
+  int i, end_i, end_t;
   ChunkBlock blk;
-  int t, t_end, seg;
+  int t, t0, t_end, seg;
   bool live;
-  __device__ Walk(const ChunkParams& params, int w) : p(params) {
-    at = p.starts[w];
-    end = p.starts[w + 1];
-    seg = -1;
-    t = 0;
-    live = false;
+  __device__ Walk(const ChunkParams& params, int w) : p(params), seg(0) {
+    const ChunkStart& start = p.starts[w];
+    const ChunkStart& end = p.starts[w + 1];
+    i = start.i;
+    t0 = start.t;
+    blk = start.blk;
+    end_i = end.i;
+    end_t = end.t;
     open();
   }
   __device__ void open() {
-    live = at.i < end.i || (at.i == end.i && at.t < end.t);
-    if (!live) return;
-    blk = p.blocks[at.i];
-    t = at.t;
-    t_end = at.i < end.i ? blk.tiles : end.t;
-    ++seg;
+    live = i < end_i || (i == end_i && t0 < end_t);
+    t = t0;
+    t_end = i < end_i ? blk.tiles : end_t;
   }
-  __device__ bool first() const { return t == at.t; }
+  __device__ bool first() const { return t == t0; }
   __device__ bool last() const { return t == t_end - 1; }
   __device__ void next_segment() {
-    at = ChunkStart{at.i + 1, 0};
+    ++i;
+    ++seg;
+    t0 = 0;
+    if (i < end_i || (i == end_i && end_t > 0)) blk = p.blocks[i];
     open();
   }
   __device__ void advance() {
@@ -450,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const bool whole = it.t_end == it.blk.tiles && it.at.t == 0;
+        const bool whole = it.t_end == it.blk.tiles && it.t0 == 0;
         const float inv = total > 0.f ? 1.f / total : total != total ? total : 0.f;  // (no key: out 0, lse -inf)
         const int in_block = 64 * rank + 32 * (warp & 1);  // first of this warp's rows
         const int slot = it.seg == 0 ? 0 : 1;

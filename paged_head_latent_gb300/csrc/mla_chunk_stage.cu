@@ -32,7 +32,8 @@ __device__ __forceinline__ ChunkReq load_request(const ChunkParams& p, int b) {
 
 // One block: the list of row blocks with their running cost, and every worker's start.
 // Blocks follow one another in row order; a block costs kBlockCost + its tiles, and worker
-// w takes the tiles whose cost units lie in [w C / G, (w + 1) C / G).
+// w takes the tiles whose cost units lie in [w C / G, (w + 1) C / G); a start in a block's
+// leading units is the block's first tile.
 __device__ void plan(const ChunkParams& p) {
   __shared__ long long part[kStageThreads / 32];
   __shared__ int near_first[kNear];
@@ -100,19 +101,32 @@ __device__ void plan(const ChunkParams& p) {
     cost += total;
   }
   __syncthreads();
+  // At most one worker for each cost unit, so that two starts inside a block are never the same.
+  const long long G = min((long long)p.workers, max(cost, 1LL));
+  auto start_of = [&](long long w) { return w < G ? w * cost / G : cost; };
   for (int w = threadIdx.x; w <= p.workers; w += kStageThreads) {
-    ChunkStart s{nblocks, 0};
-    const long long x = (long long)w * cost / p.workers;
-    if (w < p.workers && x < cost) {
+    ChunkStart s{nblocks, 0, ChunkBlock{}};
+    ChunkMerge m{0, 0, 0, 0};
+    const long long x = start_of(w);
+    if (x < cost) {
       int lo = 0, hi = nblocks - 1;  // last block whose cost0 is <= x
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (cost_of(mid) <= x) lo = mid; else hi = mid - 1;
       }
+      const long long c0 = cost_of(lo);
       s.i = lo;
-      s.t = (int)max(0LL, x - cost_of(lo) - kBlockCost);
+      s.t = (int)max(0LL, x - c0 - kBlockCost);
+      s.blk = p.blocks[lo];
+      if (s.t > 0 && start_of(w + 1) >= c0 + kBlockCost + s.blk.tiles) {  // a split block's last tile
+        m.row0 = s.blk.row0;
+        m.rows = s.blk.rows;
+        m.first = (int)(((c0 + kBlockCost + 1) * G - 1) / cost);  // the worker of the block's first tile
+        m.slot = start_of(m.first) >= c0 ? 0 : 1;  // its own first block, or one after others
+      }
     }
     p.starts[w] = s;
+    if (w < p.workers) p.merges[w] = m;
   }
 }
 
@@ -190,93 +204,71 @@ __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkP
   if (threadIdx.x < 8) p.flags[(size_t)tile * 8 + threadIdx.x] = flags[threadIdx.x];
 }
 
-// Merge of split blocks.  Block (w, y): if worker w starts inside a block and holds its last
-// tile, rows 8 y .. 8 y + 7 of that block, one warp a row: lse = log2 of the sum of the
-// fragments' 2^lse, out = their average with those weights, in worker order.
-constexpr int kMergeRows = 8;
+// Merge of split blocks.  Block (w, y): of the split block that worker w ends, if any, rows
+// 32 (y / 4) .. + 31 and columns 128 (y % 4) .. + 127.  A lane has a row and 16 columns, so a
+// fragment ([column / 4][row][4]) is read 512 contiguous bytes at a time and an output sector is
+// written whole, and a row's running maximum and sum need no other lane.  Fragments are added
+// in worker order, the next two under way.
+constexpr int kMergeThreads = 256, kMergeParts = 16;
 
-__global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p) {
+  const int w = blockIdx.x;
+  // (the plan is older than the attention kernel, whose end the wait is for)
+  const ChunkMerge blk = p.merges[w];
+  const int row = 32 * (blockIdx.y >> 2) + (threadIdx.x & 31);
+  const int col = 128 * (blockIdx.y & 3) + 16 * (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int w = blockIdx.x, lane = threadIdx.x & 31;
-  const ChunkStart s = p.starts[w], e = p.starts[w + 1];
-  if (s.t == 0 || e.i == s.i) return;  // starts a block, or the block goes on in the next worker
-  const ChunkBlock blk = p.blocks[s.i];
-  const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
   if (row >= blk.rows) return;
-  // The block's first worker: the last one that starts before the block or at its tile 0.
-  int first = w;
-  for (bool found = false; !found;) {
-    const int v = first - 1 - lane;
-    const bool before = v < 0 || p.starts[v].i < s.i || p.starts[v].t == 0;
-    const unsigned hit = __ballot_sync(0xffffffffu, before);
-    found = hit != 0;
-    first = found ? max(first - __ffs(hit), 0) : first - 32;
-  }
-  // Lane f has the f-th fragment's place and lse (-inf: no fragment) of 32 at a time.
-  float top = -INFINITY, sum = 0.f, acc[16];
+  const int n = w - blk.first + 1;
+  float top = -INFINITY, sum = 0.f, acc[16], l[2];
+  float4 x[2][4];
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int v0 = first; v0 <= w; v0 += 32) {
-    const int v = v0 + lane;
-    size_t frag = 0;
-    float l = -INFINITY;
-    if (v <= w) {
-      const ChunkStart a = p.starts[v], b = p.starts[v + 1];
-      frag = ((size_t)v * 2 + (a.i == s.i ? 0 : 1)) * kChunkRows;
-      if (a.i != b.i || a.t != b.t) l = p.part_lse[frag + row];
+  auto fetch = [&](int f, int k) {
+    if (f >= n) return;
+    const size_t frag = ((size_t)(blk.first + f) * 2 + (f == 0 ? blk.slot : 0)) * kChunkRows;
+    l[k] = p.part_lse[frag + row];
+    const float4* o = reinterpret_cast<const float4*>(p.part_o + frag * kDimCkv) + (col / 4) * kChunkRows + row;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[k][q] = o[q * kChunkRows];
+  };
+  auto add = [&](int f, int k) {
+    if (f >= n) return;
+    nan |= l[k] != l[k];
+    if (!(l[k] > -INFINITY)) return;
+    const float m = fmaxf(top, l[k]), shrink = exp2f(top - m), g = exp2f(l[k] - m);
+    top = m;
+    sum = fmaf(sum, shrink, g);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      acc[4 * q] = fmaf(acc[4 * q], shrink, g * x[k][q].x);
+      acc[4 * q + 1] = fmaf(acc[4 * q + 1], shrink, g * x[k][q].y);
+      acc[4 * q + 2] = fmaf(acc[4 * q + 2], shrink, g * x[k][q].z);
+      acc[4 * q + 3] = fmaf(acc[4 * q + 3], shrink, g * x[k][q].w);
     }
-    nan |= __any_sync(0xffffffffu, l != l);
-    float m = l;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m > top) {  // (uniform) the earlier fragments' share shrinks
-      const float shrink = exp2f(top - m);
-      sum *= shrink;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] *= shrink;
-      top = m;
-    }
-    const float weight = l > -INFINITY ? exp2f(l - top) : 0.f;
-    unsigned todo = __ballot_sync(0xffffffffu, weight > 0.f);
-    while (todo) {  // two fragments in flight
-      const int f0 = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const bool two = todo != 0;
-      const int f1 = two ? __ffs(todo) - 1 : f0;
-      const float w0 = __shfl_sync(0xffffffffu, weight, f0), w1 = __shfl_sync(0xffffffffu, weight, f1);
-      todo &= todo - 1;
-      const float4* o0 = reinterpret_cast<const float4*>(p.part_o + __shfl_sync(0xffffffffu, frag, f0) * kDimCkv) + row;
-      const float4* o1 = reinterpret_cast<const float4*>(p.part_o + __shfl_sync(0xffffffffu, frag, f1) * kDimCkv) + row;
-      float4 x[4], y[4];  // [column / 4][row]
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        x[q] = o0[(lane + 32 * q) * kChunkRows];
-        y[q] = two ? o1[(lane + 32 * q) * kChunkRows] : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      sum += w0;
-      if (two) sum += w1;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc[4 * q] = fmaf(w1, y[q].x, fmaf(w0, x[q].x, acc[4 * q]));
-        acc[4 * q + 1] = fmaf(w1, y[q].y, fmaf(w0, x[q].y, acc[4 * q + 1]));
-        acc[4 * q + 2] = fmaf(w1, y[q].z, fmaf(w0, x[q].z, acc[4 * q + 2]));
-        acc[4 * q + 3] = fmaf(w1, y[q].w, fmaf(w0, x[q].w, acc[4 * q + 3]));
-      }
-    }
+  };
+  fetch(0, 0);
+  fetch(1, 1);
+  for (int f = 0; f < n; f += 2) {
+    add(f, 0);
+    fetch(f + 2, 0);
+    add(f + 1, 1);
+    fetch(f + 3, 1);
   }
   const float inv = nan ? __int_as_float(0x7fc00000) : sum > 0.f ? 1.f / sum : 0.f;
-  __nv_bfloat16* out = p.out + ((size_t)blk.row0 + row) * kDimCkv;
+  uint32_t o[8];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[4 * q] * inv, acc[4 * q + 1] * inv);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv);
-    reinterpret_cast<uint2*>(out)[lane + 32 * q] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    o[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  if (lane == 0)
+  uint4* out = reinterpret_cast<uint4*>(p.out + ((size_t)blk.row0 + row) * kDimCkv + col);
+  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  if (col == 0)
     p.lse[(size_t)blk.row0 + row] = nan ? __int_as_float(0x7fc00000)
-                                        : sum > 0.f ? 0.69314718055994531f * top + logf(sum) : -INFINITY;
+                                        : sum > 0.f ? fmaf(top, 0.69314718055994531f, logf(sum)) : -INFINITY;
 }
 
 }  // namespace
@@ -289,8 +281,8 @@ cudaError_t launch_chunk_stage(const ChunkParams& p, cudaStream_t stream) {
 cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream) {
   // A programmatic dependent of the attention kernel: its launch overlaps that kernel's tail.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.workers, kChunkRows / kMergeRows);
-  cfg.blockDim = dim3(32 * kMergeRows);
+  cfg.gridDim = dim3(p.workers, kMergeParts);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -88,18 +88,21 @@ struct FreePages {
     const int words = (p.num_pages + 31) / 32;
     if constexpr (kNear) {
       const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-      for (int w0 = 8 * warp; w0 < words; w0 += 8 * (kPlanThreads / 32)) {  // eight words of a warp in flight
-        int32_t ref[8];
+      constexpr int kFlight = 32;  // words of a warp in flight
+      for (int w0 = kFlight * warp; w0 < words; w0 += kFlight * (kPlanThreads / 32)) {
+        int32_t ref[kFlight];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kFlight; ++k) {
           const int page = 32 * (w0 + k) + lane;
           ref[k] = page < p.num_pages ? p.ref_count[page] : 1;
         }
+        uint32_t mine = 0;  // lane k keeps word w0 + k
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kFlight; ++k) {
           const unsigned b = __ballot_sync(0xffffffffu, ref[k] <= 0);
-          if (lane == 0 && w0 + k < words) bits[w0 + k] = b;
+          if (lane == k) mine = b;
         }
+        if (lane < kFlight && w0 + lane < words) bits[w0 + lane] = mine;
       }
       __syncthreads();
     }
@@ -135,63 +138,78 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolParams p, PoolWo
   __shared__ uint32_t near_bits[kNear ? kNearWords : 1];
   __shared__ int32_t near_before[kNear ? kNearWords : 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int taken;
   const int32_t* rows = kFork ? p.children : p.rows;
   auto good_row = [&](int r) { return r >= 0 && r < p.max_rows; };
+  const long long room = (long long)p.max_blocks * p.page_size;
+  struct Entry {
+    int row, len, add, need;
+    bool ok;
+  };
+  auto examine = [&](int i) {  // all but whether an earlier entry names the row
+    Entry e{-1, 0, 0, 0, false};
+    if (i >= p.n) return e;
+    e.row = rows[i];
+    if (!good_row(e.row)) return e;
+    if constexpr (kFork) {
+      const int parent = p.parents[i];
+      e.ok = good_row(parent) && parent != e.row && p.seq_lens[e.row] == 0;
+      if (e.ok) {
+        e.len = p.seq_lens[parent];
+        e.ok = e.len >= 0 && e.len <= room;
+      }
+      if (e.ok && e.len % p.page_size != 0) {
+        e.ok = is_page(p, p.block_table[(size_t)parent * p.max_blocks + e.len / p.page_size]);
+        e.need = 1;
+      }
+    } else {
+      e.len = p.seq_lens[e.row];
+      e.add = p.new_tokens[i];
+      e.ok = e.len >= 0 && e.add >= 0 && (long long)e.len + e.add <= room;
+      if (e.ok && e.add > 0 && e.len % p.page_size != 0) {
+        // The new tokens go on in the row's last page, which has to be its own.
+        const int page = p.block_table[(size_t)e.row * p.max_blocks + e.len / p.page_size];
+        e.ok = is_page(p, page) && p.ref_count[page] == 1;
+      }
+      if (e.ok) e.need = blocks_of(e.len + e.add, p.page_size) - blocks_of(e.len, p.page_size);
+    }
+    return e;
+  };
+  if (threadIdx.x == 0) taken = 0;
   for (int i = threadIdx.x; i < p.n; i += kPlanThreads)
     if (good_row(rows[i])) w.claim[rows[i]] = 0x7fffffff;
   __syncthreads();
   for (int i = threadIdx.x; i < p.n; i += kPlanThreads)
     if (good_row(rows[i])) atomicMin(&w.claim[rows[i]], i);
+  const Entry early = examine(threadIdx.x);  // (its chain of loads overlaps the claims' round trip)
   FreePages<kNear> free(p, w, near_bits, near_before);
   const long long free_pages = free.number(part);
   __syncthreads();
-  const long long room = (long long)p.max_blocks * p.page_size;
-  long long need_run = 0, new_run = 0, taken = 0, total;
+  long long need_run = 0, new_run = 0, total;
   for (int base = 0; base < p.n; base += kPlanThreads) {
     const int i = base + threadIdx.x;
-    bool ok = false;
-    int len = 0, add = 0, need = 0;
-    if (i < p.n && good_row(rows[i]) && __ldcg(&w.claim[rows[i]]) == i) {
-      const int row = rows[i];
-      if constexpr (kFork) {
-        const int parent = p.parents[i];
-        ok = good_row(parent) && parent != row && p.seq_lens[row] == 0;
-        if (ok) {
-          len = p.seq_lens[parent];
-          ok = len >= 0 && len <= room;
-        }
-        if (ok && len % p.page_size != 0) {
-          ok = is_page(p, p.block_table[(size_t)parent * p.max_blocks + len / p.page_size]);
-          need = 1;
-        }
-      } else {
-        len = p.seq_lens[row];
-        add = p.new_tokens[i];
-        ok = len >= 0 && add >= 0 && (long long)len + add <= room;
-        if (ok && add > 0 && len % p.page_size != 0) {
-          // The new tokens go on in the row's last page, which has to be its own.
-          const int page = p.block_table[(size_t)row * p.max_blocks + len / p.page_size];
-          ok = is_page(p, page) && p.ref_count[page] == 1;
-        }
-        if (ok) need = blocks_of(len + add, p.page_size) - blocks_of(len, p.page_size);
-      }
-      if (!ok) need = 0;
-    }
+    const Entry e = base == 0 ? early : examine(i);
+    const bool ok = e.ok && __ldcg(&w.claim[e.row]) == i;
+    const int need = ok ? e.need : 0;
     const long long first = need_run + block_scan(need, part, &total);
     need_run += total;
     const bool granted = ok && (need == 0 || first + need <= free_pages);
-    const long long at = new_run + block_scan(granted ? add : 0, part, &total);
-    new_run += total;
-    block_scan(granted ? need : 0, part, &total);
-    taken += total;
+    long long at = 0;
+    if constexpr (!kFork) {
+      at = new_run + block_scan(granted ? e.add : 0, part, &total);
+      new_run += total;
+    }
+    // Granted entries that need pages are a prefix of those that need any.
+    if (granted && need > 0) atomicMax(&taken, (int)(first + need));
     if (i < p.n) {
       p.results[i] = granted ? MLA_OK : ok ? MLA_ERR_NO_PAGES : MLA_ERR_BAD_INDEX;
-      w.old_len[i] = granted ? len : -1;
+      w.old_len[i] = granted ? e.len : -1;
       w.first[i] = (int32_t)first;
       if (!kFork) p.new_indptr[i] = (int32_t)at;
     }
   }
   if (!kFork && threadIdx.x == 0) p.new_indptr[p.n] = (int32_t)new_run;
+  __syncthreads();
   free.list(taken);
 }
 
@@ -227,6 +245,7 @@ __global__ void __launch_bounds__(kApplyThreads) extend_kernel(PoolParams p, Poo
 
 // One block per pair: the parent's full pages are shared, its partial page is listed for copying.
 __global__ void __launch_bounds__(kApplyThreads) fork_kernel(PoolParams p, PoolWork w) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the page copies)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
     const int len = w.old_len[i];
@@ -281,19 +300,19 @@ __global__ void __launch_bounds__(kApplyThreads) free_kernel(PoolParams p) {
 
 // Compaction.  With L live pages, the live pages with ids >= L move, in order, to the free
 // pages with ids < L: as many of the one as of the other.
-__device__ __forceinline__ int free_before(const PoolWork& w, int page) {
-  return w.before[page >> 5] + __popc(w.bits[page >> 5] & ((1u << (page & 31)) - 1u));
+__device__ __forceinline__ int free_before(const uint32_t* bits, const int32_t* before, int page) {
+  return before[page >> 5] + __popc(bits[page >> 5] & ((1u << (page & 31)) - 1u));
 }
 
 // The j-th free page (j < the number of free pages).
-__device__ __forceinline__ int free_page(const PoolWork& w, int words, int j) {
+__device__ __forceinline__ int free_page(const uint32_t* bits, const int32_t* before, int words, int j) {
   int lo = 0, hi = words - 1;  // last word with at most j free pages before it
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (w.before[mid] <= j) lo = mid; else hi = mid - 1;
+    if (before[mid] <= j) lo = mid; else hi = mid - 1;
   }
-  uint32_t b = w.bits[lo];
-  for (int k = j - w.before[lo]; k > 0; --k) b &= b - 1;
+  uint32_t b = bits[lo];
+  for (int k = j - before[lo]; k > 0; --k) b &= b - 1;
   return 32 * lo + __ffs(b) - 1;
 }
 
@@ -315,22 +334,36 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PoolParams p
       w.before[i] = free.before[i];
     }
   if (threadIdx.x == 0) {
-    if (live < p.num_pages)
-      moves = free.before[live >> 5] + __popc(free.bits[live >> 5] & ((1u << (live & 31)) - 1u));
+    if (live < p.num_pages) moves = free_before(free.bits, free.before, live);
     p.counts[0] = live;
     p.counts[1] = moves;
   }
 }
 
+template <bool kNear>
 __global__ void __launch_bounds__(256) compact_apply_kernel(PoolParams p, PoolWork w) {
+  __shared__ uint32_t near_bits[kNear ? kNearWords : 1];
+  __shared__ int32_t near_before[kNear ? kNearWords : 1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the page copies)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int live = p.counts[0], moves = p.counts[1], words = (p.num_pages + 31) / 32;
+  const uint32_t* bits = w.bits;
+  const int32_t* before = w.before;
+  if constexpr (kNear) {  // the searches below are chains of dependent reads
+    for (int i = threadIdx.x; i < words; i += blockDim.x) {
+      near_bits[i] = w.bits[i];
+      near_before[i] = w.before[i];
+    }
+    __syncthreads();
+    bits = near_bits;
+    before = near_before;
+  }
   const long long tid = blockIdx.x * blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
-  auto is_free = [&](int page) { return (w.bits[page >> 5] >> (page & 31)) & 1u; };
-  auto move_of = [&](int page) { return page - free_before(w, page) - (live - moves); };  // of a live page >= live
+  auto is_free = [&](int page) { return (bits[page >> 5] >> (page & 31)) & 1u; };
+  auto move_of = [&](int page) { return page - free_before(bits, before, page) - (live - moves); };  // of a live page >= live
   for (long long page = live + tid; page < p.num_pages; page += step) {
     if (is_free((int)page)) continue;
-    const int j = move_of((int)page), to = free_page(w, words, j);
+    const int j = move_of((int)page), to = free_page(bits, before, words, j);
     p.src[j] = (int)page;
     p.dst[j] = to;
     p.ref_count[to] = p.ref_count[page];
@@ -343,7 +376,7 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(PoolParams p, PoolWo
     if (k >= blocks_of(p.seq_lens[row], p.page_size)) continue;
     const int page = p.block_table[c];
     if (page < live || page >= p.num_pages || is_free(page)) continue;
-    p.block_table[c] = free_page(w, words, move_of(page));
+    p.block_table[c] = free_page(bits, before, words, move_of(page));
   }
 }
 
@@ -410,7 +443,9 @@ cudaError_t launch_pages_compact(const PoolParams& p, const PoolWork& w, cudaStr
   else compact_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(p, w);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long threads = (long long)p.max_rows * p.max_blocks > p.num_pages ? (long long)p.max_rows * p.max_blocks : p.num_pages;
-  return launch_apply(compact_apply_kernel, grid_of(threads, 256, 1216), 256, p, w, stream);
+  const int grid = grid_of(threads, 256, 1216);
+  return near_pool(p) ? launch_apply(compact_apply_kernel<true>, grid, 256, p, w, stream)
+                      : launch_apply(compact_apply_kernel<false>, grid, 256, p, w, stream);
 }
 
 }  // namespace mla

@@ -255,16 +255,27 @@ int mla_paged_decode_noalloc(const void* q_nope, const void* q_pe, const void* c
 int mla_noalloc_read_status(void* stream);
 
 /*
- * Causal prefill of a chunk of new tokens over an FP8 KV cache: mla_paged_prefill's
- * arguments and mask with the cache of mla_paged_decode_fp8 (every latent value read as
- * the same BF16 number).  Chunks may be ragged, down to one token or none per request;
- * rows of requests with fewer keys than queries that see no key get out = 0, lse = -inf.
- * dims->total_q may be larger than qo_indptr[batch]: the rows behind the last request are
- * left as they were.  A listed slot outside the cache is not a key.
- *   workspace >= mla_workspace_bytes_prefill_fp8(dims) bytes, zero-filled before its first
- *   use; besides the prefill's scratch it holds the call's keys as bf16 rows (1156 bytes
- *   for each of dims->num_kv_indices).
+ * Causal prefill of a chunk of new tokens with staged keys: mla_paged_prefill's arguments,
+ * mask and definition (the results differ in rounding).  The call first copies the keys it
+ * needs into its workspace, so every page size and slot order runs at the same rate, and
+ * attends in blocks of 128 (token, head) rows, so few heads cost no more than many.  Chunks
+ * may be ragged, down to one token or none per request; rows that see no key get out = 0,
+ * lse = -inf.  dims->total_q may be larger than qo_indptr[batch], and num_kv_indices than
+ * kv_indptr[batch]: the rows behind the last request are left as they were.  (MLA_VALIDATE
+ * reports both, as for mla_paged_prefill.)  A listed slot outside the cache is not a key.
+ * A key that holds a value that is not finite makes out and lse NaN in the rows that see
+ * it and changes no other row.
+ *   workspace >= mla_workspace_bytes_prefill_staged(dims) bytes, zero-filled before its first
+ *   use; it holds the staged keys (1152 bytes for each of dims->num_kv_indices, plus up to
+ *   128 keys per request) and one 256 KB fragment pair per worker.
+ * mla_paged_prefill_fp8 is the same over the FP8 cache of mla_paged_decode_fp8 (every latent
+ * value read as the same BF16 number), with the same workspace size.
  */
+size_t mla_workspace_bytes_prefill_staged(const mla_dims* dims);
+int mla_paged_prefill_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                             const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices,
+                             float sm_scale, void* out, float* lse, const mla_dims* dims, void* workspace,
+                             size_t workspace_bytes, int flags, void* stream);
 size_t mla_workspace_bytes_prefill_fp8(const mla_dims* dims);
 int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
                           const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out,

@@ -82,6 +82,10 @@ _SIGNATURES = [
       ctypes.c_int, _P]),
     ("mla_paged_decode_noalloc", ctypes.c_int,
      [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), ctypes.c_int, _P]),
+    ("mla_workspace_bytes_prefill_staged", ctypes.c_size_t, [ctypes.POINTER(MlaDims)]),
+    ("mla_paged_prefill_staged", ctypes.c_int,
+     [_P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P, ctypes.c_size_t,
+      ctypes.c_int, _P]),
     ("mla_workspace_bytes_prefill_fp8", ctypes.c_size_t, [ctypes.POINTER(MlaDims)]),
     ("mla_paged_prefill_fp8", ctypes.c_int,
      [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P, ctypes.c_size_t, ctypes.c_int,
@@ -633,8 +637,8 @@ def run_workload(w, out=None, lse=None, workspace=None, flags=0, num_workers=0, 
                              w.kv_indices, w.sm_scale, out, lse, workspace, flags, num_workers, stream)
 
 
-# The cache's writers and readers, the FP8 chunk prefill and the page pool.
+# The cache's writers and readers, the staged chunk prefill and the page pool.
 from .cache import (mla_cache_copy_pages, mla_cache_copy_pages_fp8, mla_cache_gather,  # noqa: E402
-                    mla_cache_gather_fp8, mla_paged_prefill_fp8, mla_pages_compact, mla_pages_extend,
-                    mla_pages_fork, mla_pages_free, mla_rope_append, mla_rope_append_fp8, workspace_bytes_pages,
-                    workspace_bytes_prefill_fp8)
+                    mla_cache_gather_fp8, mla_paged_prefill_fp8, mla_paged_prefill_staged, mla_pages_compact,
+                    mla_pages_extend, mla_pages_fork, mla_pages_free, mla_rope_append, mla_rope_append_fp8,
+                    workspace_bytes_pages, workspace_bytes_prefill_fp8, workspace_bytes_prefill_staged)

@@ -1,4 +1,4 @@
-"""Binding of the cache's writers and readers, the FP8 chunk prefill and the page pool.
+"""Binding of the cache's writers and readers, the staged chunk prefill and the page pool.
 
 Argument checks and marshalling only, like the package's other calls (include/mla_paged.h
 has the definitions).  Every tensor is on one CUDA device, the call runs there on ``stream``
@@ -232,18 +232,17 @@ def mla_cache_copy_pages_fp8(kv_fp8, src, dst, tokens=None, count=None, stream=N
                 count, stream)
 
 
-# ---------------------------------------------------------------- the FP8 chunk prefill
+# ---------------------------------------------------------------- the staged chunk prefill
+def workspace_bytes_prefill_staged(dims: MlaDims) -> int:
+    return int(lib().mla_workspace_bytes_prefill_staged(ctypes.byref(dims)))
+
+
 def workspace_bytes_prefill_fp8(dims: MlaDims) -> int:
     return int(lib().mla_workspace_bytes_prefill_fp8(ctypes.byref(dims)))
 
 
-def mla_paged_prefill_fp8(q_nope, q_pe, kv_fp8, qo_indptr, kv_indptr, kv_indices, sm_scale, out=None, lse=None,
-                          workspace=None, flags=0, num_workers=0,
-                          stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Causal attention (bottom-right aligned) of a chunk of new tokens over an FP8 cache:
-    ``mla_paged_prefill`` with kv_fp8 [num_pages, page_size, 656].  Returns (out, lse); rows
-    behind qo_indptr's last request are left as they were."""
-    _check("q_nope", q_nope, _BF16)
+def _prefill(name, q_nope, q_pe, cache, geometry, qo_indptr, kv_indptr, kv_indices, sm_scale, out, lse, workspace, flags,
+             num_workers, stream):
     index = q_nope.get_device()
     _check("q_pe", q_pe, _BF16, index)
     if q_nope.dim() != 3:
@@ -251,26 +250,48 @@ def mla_paged_prefill_fp8(q_nope, q_pe, kv_fp8, qo_indptr, kv_indptr, kv_indices
     rows, heads = q_nope.shape[0], q_nope.shape[1]
     if q_nope.shape != (rows, heads, HEAD_DIM_CKV) or q_pe.shape != (rows, heads, HEAD_DIM_KPE):
         raise ValueError("q_nope must be [total_q, H, 512] and q_pe [total_q, H, 64]")
-    num_pages, page_size = _fp8_cache(kv_fp8, index)
     _check("qo_indptr", qo_indptr, _I32, index)
     _check("kv_indptr", kv_indptr, _I32, index)
     _check("kv_indices", kv_indices, _I32, index)
     batch = kv_indptr.numel() - 1
     if batch < 0 or qo_indptr.numel() != batch + 1:
         raise ValueError("qo_indptr and kv_indptr must both have batch + 1 entries")
-    dims = make_dims(batch, heads, num_pages, page_size, kv_indices.numel(), total_q=rows, num_workers=num_workers)
+    dims = make_dims(batch, heads, geometry[0], geometry[1], kv_indices.numel(), total_q=rows, num_workers=num_workers)
     out = _buffer("out", out, (rows, heads, HEAD_DIM_CKV), _BF16, q_nope)
     lse = _buffer("lse", lse, (rows, heads), _F32, q_nope)
     if workspace is None:
         with torch.cuda.device(index):
-            need = workspace_bytes_prefill_fp8(dims)
-        workspace = _scratch(None, need, q_nope, "mla_workspace_bytes_prefill_fp8")
+            need = workspace_bytes_prefill_staged(dims)
+        workspace = _scratch(None, need, q_nope, "mla_workspace_bytes_prefill_staged")
     else:  # (the library checks its size)
         _check("workspace", workspace, _U8, index)
-    _call("mla_paged_prefill_fp8", index, stream, q_nope.data_ptr(), q_pe.data_ptr(), kv_fp8.data_ptr(),
-          qo_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), sm_scale, out.data_ptr(), lse.data_ptr(),
-          ctypes.byref(dims), workspace.data_ptr(), workspace.numel(), flags)
+    _call(name, index, stream, q_nope.data_ptr(), q_pe.data_ptr(), *cache, qo_indptr.data_ptr(), kv_indptr.data_ptr(),
+          kv_indices.data_ptr(), sm_scale, out.data_ptr(), lse.data_ptr(), ctypes.byref(dims), workspace.data_ptr(),
+          workspace.numel(), flags)
     return out, lse
+
+
+def mla_paged_prefill_staged(q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, kv_indptr, kv_indices, sm_scale, out=None,
+                             lse=None, workspace=None, flags=0, num_workers=0,
+                             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention (bottom-right aligned) of a chunk of new tokens: what
+    ``mla_paged_prefill`` computes, with the keys staged in the workspace and the query rows
+    (token, head) in blocks of 128.  Returns (out, lse); rows behind qo_indptr's last request
+    are left as they were."""
+    _check("q_nope", q_nope, _BF16)
+    geometry = _bf16_caches(ckv_cache, kpe_cache, q_nope.get_device())
+    return _prefill("mla_paged_prefill_staged", q_nope, q_pe, (ckv_cache.data_ptr(), kpe_cache.data_ptr()), geometry,
+                    qo_indptr, kv_indptr, kv_indices, sm_scale, out, lse, workspace, flags, num_workers, stream)
+
+
+def mla_paged_prefill_fp8(q_nope, q_pe, kv_fp8, qo_indptr, kv_indptr, kv_indices, sm_scale, out=None, lse=None,
+                          workspace=None, flags=0, num_workers=0,
+                          stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``mla_paged_prefill_staged`` over an FP8 cache kv_fp8 [num_pages, page_size, 656]."""
+    _check("q_nope", q_nope, _BF16)
+    geometry = _fp8_cache(kv_fp8, q_nope.get_device())
+    return _prefill("mla_paged_prefill_fp8", q_nope, q_pe, (kv_fp8.data_ptr(),), geometry, qo_indptr, kv_indptr,
+                    kv_indices, sm_scale, out, lse, workspace, flags, num_workers, stream)
 
 
 # ---------------------------------------------------------------- the page pool

@@ -39,7 +39,9 @@ struct ChunkParams {
   const int32_t* qo_indptr;
   const int32_t* kv_indptr;
   const int32_t* kv_indices;
-  const uint8_t* kv_fp8;
+  const uint8_t* kv_fp8;            // FP8 cache, or
+  const __nv_bfloat16* ckv_cache;   // bf16 caches
+  const __nv_bfloat16* kpe_cache;
   __nv_bfloat16* out;  // [total_q * H, 512]
   float* lse;          // [total_q * H]
   int batch, heads, total_q, num_slots, num_kv_indices, workers;
@@ -85,7 +87,7 @@ struct ChunkLayout {
 };
 
 // The three launches of a call: stage the keys and plan, attend, merge split blocks.
-cudaError_t launch_chunk_stage(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_stage(const ChunkParams& p, bool fp8, cudaStream_t stream);
 cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream);
 

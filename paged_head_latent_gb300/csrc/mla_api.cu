@@ -407,26 +407,23 @@ bool block_table_dims(const mla_dims* dims, int max_blocks, mla_dims* d) {
 }
 }  // namespace
 
-extern "C" {
+namespace {
 
-size_t mla_workspace_bytes_prefill_fp8(const mla_dims* dims) {
-  if (check_dims(dims, true) != MLA_OK) return 0;
-  int G = 0;
-  if (resolve_workers(dims, &G) != MLA_OK) return 0;
-  return mla::ChunkLayout(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices).total;
-}
-
-int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
-                          const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out, float* lse,
-                          const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream_ptr) {
+// The staged prefill: keys as bf16 tiles in the workspace, then blocks of 128 query rows.
+int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache, const void* kv_fp8,
+               bool fp8, const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale,
+               void* out, float* lse, const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags,
+               void* stream_ptr) {
   int st = check_dims(dims, true);
   if (st != MLA_OK) return st;
   if (!std::isfinite(sm_scale)) return MLA_ERR_DIMS;
   if (dims->total_q == 0 || dims->batch == 0) return MLA_OK;
   if (!q_nope || !q_pe || !qo_indptr || !kv_indptr || !out || !lse) return MLA_ERR_NULL;
   if (dims->num_kv_indices > 0 && !kv_indices) return MLA_ERR_NULL;
-  if (dims->num_pages > 0 && !kv_fp8) return MLA_ERR_NULL;
-  if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(kv_fp8) || !aligned16(out)) return MLA_ERR_ALIGN;
+  if (dims->num_pages > 0 && (fp8 ? !kv_fp8 : !ckv_cache || !kpe_cache)) return MLA_ERR_NULL;
+  if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(ckv_cache) || !aligned16(kpe_cache) || !aligned16(kv_fp8) ||
+      !aligned16(out))
+    return MLA_ERR_ALIGN;
   int G = 0;
   if ((st = resolve_workers(dims, &G)) != MLA_OK) return st;
   const mla::ChunkLayout lay(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices);
@@ -444,6 +441,8 @@ int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_f
   p.kv_indptr = kv_indptr;
   p.kv_indices = kv_indices;
   p.kv_fp8 = static_cast<const uint8_t*>(kv_fp8);
+  p.ckv_cache = static_cast<const __nv_bfloat16*>(ckv_cache);
+  p.kpe_cache = static_cast<const __nv_bfloat16*>(kpe_cache);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.batch = dims->batch;
@@ -491,10 +490,38 @@ int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_f
     v.status = p.status;
     if (mla::launch_validate(v, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
   }
-  if (mla::launch_chunk_stage(p, stream) != cudaSuccess || mla::launch_chunk(maps, p, stream) != cudaSuccess ||
+  if (mla::launch_chunk_stage(p, fp8, stream) != cudaSuccess || mla::launch_chunk(maps, p, stream) != cudaSuccess ||
       mla::launch_chunk_merge(p, stream) != cudaSuccess)
     return MLA_ERR_LAUNCH;
   return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mla_workspace_bytes_prefill_staged(const mla_dims* dims) {
+  if (check_dims(dims, true) != MLA_OK) return 0;
+  int G = 0;
+  if (resolve_workers(dims, &G) != MLA_OK) return 0;
+  return mla::ChunkLayout(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices).total;
+}
+
+int mla_paged_prefill_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                             const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices,
+                             float sm_scale, void* out, float* lse, const mla_dims* dims, void* workspace,
+                             size_t workspace_bytes, int flags, void* stream) {
+  return run_staged(q_nope, q_pe, ckv_cache, kpe_cache, nullptr, false, qo_indptr, kv_indptr, kv_indices, sm_scale, out,
+                    lse, dims, workspace, workspace_bytes, flags, stream);
+}
+
+size_t mla_workspace_bytes_prefill_fp8(const mla_dims* dims) { return mla_workspace_bytes_prefill_staged(dims); }
+
+int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
+                          const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out, float* lse,
+                          const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream) {
+  return run_staged(q_nope, q_pe, nullptr, nullptr, kv_fp8, true, qo_indptr, kv_indptr, kv_indices, sm_scale, out, lse,
+                    dims, workspace, workspace_bytes, flags, stream);
 }
 
 }  // extern "C"

@@ -131,10 +131,11 @@ __device__ void plan(const ChunkParams& p) {
 }
 
 // One block per staged tile (and one more for the plan): 128 keys of one request, read
-// through their slots, dequantised to the bf16 numbers that the cache stands for.  Rows past
+// through their slots, as the bf16 numbers that the cache holds or (kFp8) stands for.  Rows past
 // the request's keys, slots outside the cache and keys with a value that is not finite
 // are written as zeros, so that a weight of zero always makes a zero product; the tile's
 // flags tell which rows are keys and which of them were not finite.
+template <bool kFp8>
 __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) {
@@ -168,23 +169,36 @@ __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkP
   if (threadIdx.x < 8) flags[threadIdx.x] = 0;
   __syncthreads();
   if (mine >= p.num_slots) mine = -1;
-  uint4 code[kTok], rope[kTok];
+  uint4 lat[kTok][kFp8 ? 1 : 2], rope[kTok];  // lane: latent values 16 lane .. + 15, rope values 8 lane .. + 7
   float sc[kTok];
 #pragma unroll
   for (int k = 0; k < kTok; ++k) {
     const int slot = __shfl_sync(0xffffffffu, mine, k);
-    code[k] = rope[k] = make_uint4(0, 0, 0, 0);
+    lat[k][0] = lat[k][kFp8 ? 0 : 1] = rope[k] = make_uint4(0, 0, 0, 0);
     sc[k] = 0.f;
     if (slot < 0) continue;
-    const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
-    code[k] = *reinterpret_cast<const uint4*>(tok + 16 * lane);
-    sc[k] = *reinterpret_cast<const float*>(tok + kDimCkv + 4 * (lane >> 3));
-    if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
+    if constexpr (kFp8) {
+      const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
+      lat[k][0] = *reinterpret_cast<const uint4*>(tok + 16 * lane);
+      sc[k] = *reinterpret_cast<const float*>(tok + kDimCkv + 4 * (lane >> 3));
+      if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
+    } else {
+      const uint4* tok = reinterpret_cast<const uint4*>(p.ckv_cache + (size_t)slot * kDimCkv + 16 * lane);
+      lat[k][0] = tok[0];
+      lat[k][1] = tok[1];
+      if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * lane);
+    }
   }
 #pragma unroll
   for (int k = 0; k < kTok; ++k) {
-    uint4 a = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(code[k].x, code[k].y), sc[k]);
-    uint4 b = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(code[k].z, code[k].w), sc[k]);
+    uint4 a, b;
+    if constexpr (kFp8) {
+      a = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(lat[k][0].x, lat[k][0].y), sc[k]);
+      b = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(lat[k][0].z, lat[k][0].w), sc[k]);
+    } else {
+      a = lat[k][0];
+      b = lat[k][1];
+    }
     const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, rope[k].x, rope[k].y, rope[k].z, rope[k].w};
     uint32_t odd = 0;
 #pragma unroll
@@ -273,8 +287,9 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
 
 }  // namespace
 
-cudaError_t launch_chunk_stage(const ChunkParams& p, cudaStream_t stream) {
-  chunk_stage_kernel<<<p.tiles + 1, kStageThreads, 0, stream>>>(p);
+cudaError_t launch_chunk_stage(const ChunkParams& p, bool fp8, cudaStream_t stream) {
+  if (fp8) chunk_stage_kernel<true><<<p.tiles + 1, kStageThreads, 0, stream>>>(p);
+  else chunk_stage_kernel<false><<<p.tiles + 1, kStageThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

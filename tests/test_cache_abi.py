@@ -141,5 +141,26 @@ def test_prefill_fp8_refusals(lib):
     assert _prefill(lib, dims(), ws=FAKE + 8) == ALIGN
     assert _prefill(lib, dims(total_q=0)) == 0
     small, large = (lib.workspace_bytes_prefill_fp8(dims(num_kv_indices=n)) for n in (64, 6400))
-    assert large - small >= 1152 * (6400 - 64)
+    assert large - small >= 1152 * (6400 - 128)
     assert lib.workspace_bytes_prefill_fp8(dims(num_qo_heads=0)) == 0
+
+
+def test_prefill_staged_refusals(lib):
+    dims = lib.make_dims(2, 16, 4, 64, 10, total_q=3, num_workers=4)
+    names = ["q_nope", "q_pe", "ckv", "kpe", "qo", "kp", "ki", "out", "lse"]
+
+    def call(null=None, off=None, d=dims, ws=FAKE, size=1 << 40, scale=0.1):
+        p = [V(0 if n == null else FAKE + (8 if n == off else 0)) for n in names]
+        return lib.lib().mla_paged_prefill_staged(*p[:7], scale, *p[7:], ctypes.byref(d), V(ws), size, 0, None)
+
+    for n in names:
+        assert call(null=n) == NULL, n
+    for n in ("q_nope", "q_pe", "ckv", "kpe", "out"):
+        assert call(off=n) == ALIGN, n
+    assert call(scale=float("nan")) == DIMS
+    assert call(ws=0) == WORKSPACE and call(size=4096) == WORKSPACE and call(ws=FAKE + 8) == ALIGN
+    assert call(d=lib.make_dims(2, 16, 4, 64, 10, total_q=0)) == 0
+    assert call(d=lib.make_dims(0, 16, 4, 64, 0, total_q=5)) == 0
+    # Staged rows are 32-bit coordinates: too many requests or keys are refused.
+    assert call(d=lib.make_dims(1 << 24, 1, 4, 64, 10, total_q=3, num_workers=4)) == DIMS
+    assert lib.workspace_bytes_prefill_staged(dims) == lib.workspace_bytes_prefill_fp8(dims)

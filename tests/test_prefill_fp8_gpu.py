@@ -188,6 +188,190 @@ def test_repeats_exactly(lib):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def bf16_caches(x):
+    ckv, kpe = oracle.dequantize_fp8_cache(x["kv"].numpy())
+    shape = x["kv"].shape[:2]
+    return (torch.from_numpy(np.asarray(ckv)).reshape(*shape, 512).to(torch.bfloat16).cuda(),
+            torch.from_numpy(np.asarray(kpe)).reshape(*shape, 64).to(torch.bfloat16).cuda())
+
+
+@pytest.mark.parametrize("heads,page", [(1, 1), (16, 64), (100, 7), (128, 128)])
+def test_staged_prefill_of_the_bf16_cache_is_the_same_bits(lib, heads, page):
+    """The FP8 form stages the very numbers that the dequantised bf16 cache holds."""
+    require_gpu()
+    x = make([3, 0, 40, 1], [150, 9, 40, 700], heads, page, seed=20 + heads)
+    x["ki"][5], x["ki"][160] = -3, 2 ** 31 - 1
+    a = run(lib, x)
+    c = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    b = lib.mla_paged_prefill_staged(c["qn"], c["qp"], *bf16_caches(x), c["qo"], c["kp"], c["ki"], x["scale"])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    close(b, plain(x))
+
+
+def test_staged_prefill_agrees_with_the_row_by_row_prefill(lib):
+    """Both within their bounds of the exact values, so within the sum of their bounds."""
+    require_gpu()
+    w = wl.make_prefill([33, 70, 1], [31, 0, 500], num_qo_heads=128, page_size=64, seed=99, name="staged").to("cuda")
+    a = lib.run_workload(w)
+    b = lib.mla_paged_prefill_staged(w.q_nope, w.q_pe, w.ckv_cache, w.kpe_cache, w.qo_indptr, w.kv_indptr, w.kv_indices,
+                                     w.sm_scale)
+    # 2^-8 (|ref| + W) each, W <= max |v| < 5.5; lse within 1e-3 of the row-by-row kernel's tolerance
+    assert (a[0].float() - b[0].float()).abs().max() <= 4 * 2.0 ** -8 * 5.5
+    assert (a[1] - b[1]).abs().max() <= 1e-3
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("workers", [0, 5])
+def test_keys_that_are_not_finite(lib, heads, workers):
+    """A NaN or infinite key makes the rows that see it NaN and no other: not the earlier tokens
+    of the same block, not the other requests, not rows that end on the same tile."""
+    require_gpu()
+    x = make([6, 9, 4], [130, 300, 64], heads, 64, seed=30)
+    tokens = x["kv"].view(-1, 656)
+    keys = {b: x["ki"][x["kp"][b]:x["kp"][b + 1]].long() for b in range(3)}
+    clean = plain(x)
+    # Request 0: its last token's key has a NaN code, so only that token sees it.  Request 1: a
+    # scale is infinite on the key of its token 5.  Request 2: an infinite rope value on key 0.
+    tokens[keys[0][129], 100] = 0x7F
+    tokens[keys[1][296], 512:516] = torch.tensor([float("inf")]).view(torch.uint8)
+    tokens[keys[2][0], 528:530] = torch.tensor([float("-inf")], dtype=torch.bfloat16).view(torch.uint8)
+    out, lse = (t.float().cpu() for t in run(lib, x, num_workers=workers))
+    bad = torch.zeros(19, dtype=torch.bool)
+    bad[5] = True            # request 0, token 5
+    bad[6 + 5:15] = True     # request 1, tokens 5 .. 8 see key 296
+    bad[15:] = True          # request 2, every token
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    good = ~bad.numpy()
+    close((out[~bad], lse[~bad]), tuple(t[good] for t in clean))
+
+
+def test_queries_that_are_not_finite(lib):
+    """A NaN query row spoils that row alone, not the rows of its block."""
+    require_gpu()
+    x = make([7, 5], [90, 200], 24, 16, seed=31)
+    ref = plain(x)
+    x["qn"][3, 7, 11] = float("nan")
+    x["qp"][8, 0, 5] = float("inf")
+    out, lse = (t.float().cpu() for t in run(lib, x))
+    bad = torch.zeros(12, 24, dtype=torch.bool)
+    bad[3, 7] = bad[8, 0] = True
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    good = ~bad.numpy()
+    close((out[~bad], lse[~bad]), tuple(t[good] for t in ref))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1e-30, 3.0])
+def test_softmax_scales(lib, scale):
+    require_gpu()
+    x = make([9, 2], [140, 77], 16, 64, seed=32)
+    x["scale"] = scale
+    ref = list(plain(x))
+    ref[3] = np.abs(ref[3])
+    close(run(lib, x), ref)
+
+
+def test_same_slot_many_times(lib):
+    require_gpu()
+    x = make([8, 3], [200, 64], 16, 64, seed=33)
+    x["ki"][:200] = x["ki"][:200][torch.arange(200) % 7]
+    close(run(lib, x), plain(x))
+
+
+def test_two_streams_with_their_own_workspaces(lib):
+    require_gpu()
+    xs = [make([60, 9], [500, 130], 16, 64, seed=40 + i) for i in range(2)]
+    refs = [plain(x) for x in xs]
+    on_gpu = [{k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()} for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    ws = [torch.zeros(1 << 27, dtype=torch.uint8, device="cuda") for _ in xs]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs = [lib.mla_paged_prefill_fp8(c["qn"], c["qp"], c["kv"], c["qo"], c["kp"], c["ki"], c["scale"], workspace=w,
+                                          stream=s) for c, w, s in zip(on_gpu, ws, streams)]
+    torch.cuda.synchronize()
+    for o, r in zip(outs, refs):
+        close(o, r)
+
+
+def test_validate_reports_bad_offsets(lib):
+    require_gpu()
+    x = make([4, 7], [200, 70], 16, 64, seed=34)
+    ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+    run(lib, x, workspace=ws, flags=lib.MLA_VALIDATE)
+    assert lib.read_device_status(ws) == 0
+    x["ki"][3] = -1
+    run(lib, x, workspace=ws, flags=lib.MLA_VALIDATE)
+    assert lib.read_device_status(ws) == -6
+
+
+@pytest.mark.parametrize("qo,kp", [([0, 11, 4], [0, 200, 270]), ([0, 4, 11], [0, 300, 270]), ([5, 2, 60], [-7, 900, 3]),
+                                   ([0, 11, 0], [0, 270, 0])])
+def test_corrupt_offsets_stay_in_bounds(lib, qo, kp):
+    """Offsets that decrease or leave their arrays: the call returns, and nothing outside the
+    outputs is written (guard rows keep their values)."""
+    require_gpu()
+    x = make([4, 7], [200, 70], 16, 64, seed=35)
+    x["qo"], x["kp"] = torch.tensor(qo, dtype=torch.int32), torch.tensor(kp, dtype=torch.int32)
+    guard = torch.full((11 + 64, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((11 + 64, 16), 7.0, device="cuda")
+    run(lib, x, out=guard[32:43], lse=lse[32:43])
+    torch.cuda.synchronize()
+    for t in (guard, lse):
+        assert (t[:32] == 7).all() and (t[43:] == 7).all()
+
+
+def test_bounded_waits(lib):
+    """A load that never happens: the call returns, the status says timeout, the next call is right."""
+    require_gpu()
+    x = make([40], [2000], 16, 64, seed=36)
+    ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    try:
+        lib.lib().mla_debug_inject_timeout(1, 20_000_000)
+        run(lib, x, workspace=ws, num_workers=1)
+        assert lib.read_device_status(ws) == -7
+    finally:
+        lib.lib().mla_debug_inject_timeout(-1, 0)
+    close(run(lib, x, workspace=ws, num_workers=1), plain(x))
+    assert lib.read_device_status(ws) == 0
+
+
+def test_long_cache(lib):
+    """2.1 million keys of one request: staged rows past 2 GB, a row split over every worker."""
+    require_gpu()
+    n, page = 2_100_000, 64
+    pages = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kv = torch.zeros(pages, page, 656, dtype=torch.uint8, device="cuda")
+    kv[..., :512] = torch.randint(0, 0x7F, (pages, page, 512), generator=g, device="cuda", dtype=torch.uint8)
+    kv[..., 512:528] = torch.full((4,), 2.0 ** -6, device="cuda").view(torch.uint8)
+    kv[..., 528:] = torch.randn(pages, page, 64, generator=g, device="cuda").to(torch.bfloat16).view(torch.uint8)
+    q = [torch.randn(3, 5, d, generator=g, device="cuda").to(torch.bfloat16) for d in (512, 64)]
+    ki = torch.randperm(pages * page, generator=g, device="cuda")[:n].to(torch.int32)
+    scale = 0.02
+    out, lse = lib.mla_paged_prefill_fp8(*q, kv, torch.tensor([0, 3], dtype=torch.int32, device="cuda"),
+                                         torch.tensor([0, n], dtype=torch.int32, device="cuda"), ki, scale)
+    tok = kv.view(-1, 656)
+    top, acc, tot, wsum = None, 0, 0, 0
+    for at in range(0, n, 300_000):
+        rows = tok[ki[at:at + 300_000].long()]
+        v = rows[:, :512].contiguous().view(torch.float8_e4m3fn).double() * 2.0 ** -6
+        r = rows[:, 528:].contiguous().view(torch.bfloat16).double()
+        s = (q[0].double() @ v.t() + q[1].double() @ r.t()) * scale
+        idx = torch.arange(at, at + rows.shape[0], device="cuda")
+        s = s.masked_fill((idx[None] >= (n - 3 + torch.arange(3, device="cuda") + 1)[:, None])[:, None], -math.inf)
+        m = s.amax(-1, keepdim=True) if top is None else torch.maximum(top, s.amax(-1, keepdim=True))
+        old = 1.0 if top is None else torch.exp(top - m)
+        p = torch.exp(s - m)
+        acc, tot, wsum = acc * old + p @ v, tot * old + p.sum(-1, keepdim=True), wsum * old + p @ v.abs()
+        top = m
+    ref, w = acc / tot, wsum / tot
+    assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 1e-3) * w).all()
+    # (float32 sums of 2.1 million terms in tiles: 2^-24 for each of at most 220 partial sums a worker)
+    assert ((lse.double() - (top + tot.log())[..., 0]).abs() <= 1e-4).all()
+
+
 def test_serving_steps_end_to_end(lib):
     """The operators as a serving program chains them: prompts extend the pool, are rotated
     and written, attend as a chunk; a fork, its page copies, a decode step, a free and a

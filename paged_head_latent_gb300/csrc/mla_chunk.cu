@@ -12,17 +12,22 @@
 // 256 columns (lanes 0-63 hold the first half of the product's columns, lanes 64-127 the
 // second), two S tiles 64 columns each, and the softmax of a row never leaves its SM.  The
 // B operand is split instead: SM c stages 64 of a tile's 128 keys (all 576 columns) for S and
-// all 128 keys of its 256 latent columns for O.  Measured on this part: M = 128, N = 256 runs
-// at the full rate (65 cycles a 16-deep step), N = 128 at 46 cycles (not 32), so a tile costs
-// 36 x 46 + 16 x 65 = 2696 cycles of the tensor pipe, 81 % of the peak rate.  One SM alone
-// (cta_group::1) has half the rate at M = 64, and a key-split of the depth needs partial
-// scores to cross between the SMs (the decode kernel's way), which bounds it at 45 %.
+// all 128 keys of its 256 latent columns for O.  Measured on this part: a 16-deep step takes
+// 32.2 cycles for S (N = 128) and 64.3 for O (N = 256), the full rate, so a tile costs 36 x 32 +
+// 16 x 64 = 2176 cycles of the tensor pipe; one SM alone (cta_group::1) has half the rate at M =
+// 64, and a split of the depth needs partial scores to cross between the SMs (the decode
+// kernel's way; its prefill runs at 0.45 of this rate).
 //
 // Shared memory (224 KB): Q (64 rows x 576, 72 KB), one K tile (9 chunks of 64 keys x 64
 // columns, 8 KB each), one V tile (8 such chunks) and P (16 KB).  Nothing is double-buffered:
-// every chunk has its own barrier and is reloaded as soon as the products that read it are
-// done, which leaves each load about 2400 of the tile's cycles.  The loads are 136 KB per SM
-// and tile, 50 bytes a cycle; L2 sustained 62 bytes a cycle and SM for these boxes.
+// K is reloaded in three parts and V in two, each as soon as the products that read it are
+// done, which leaves a load most of a tile's time.  The loads are 136 KB per SM and tile; L2
+// sustained 62 bytes a cycle and SM for these boxes, which is 2250 cycles a tile.
+//
+// What bounds it.  A tile takes 2470 cycles with its share of the blocks' starts and ends (four
+// prompts, 128 heads, 22 tiles a block: 870 us, 1.72 PFLOP/s, 0.90 of the measured bf16 burst rate, at
+// the 1.6 GHz that the power limit leaves; one prompt of 256 tokens over 4096 keys: tensor pipe
+// 80 % active).  Shared memory is the next limit: operands, loads and P move 392 KB a tile.
 //
 // The tensor pipe's order is S(j+1), then O += P(j) V(j): the softmax of tile j runs while S(j+1)
 // is computed.

@@ -82,7 +82,8 @@ struct PoolParams {
 // Scratch of one call; nothing in it outlives the call.
 struct PoolWork {
   uint32_t* bits;            // free pages, 32 a word
-  int32_t* before;           // free pages before a word
+  int32_t* before;           // free pages before a word (in a large pool: within its span)
+  int32_t* base;             // free pages before a span of words (large pools)
   int32_t* claim;            // [max_rows] first entry that names the row
   int32_t* pages;            // [num_pages] the free pages that the call takes
   int32_t* old_len;          // [n] length that a granted entry starts from, else -1

@@ -3,8 +3,8 @@
 // HBM (a few operations per byte) or, for a few tokens, by the launch.
 //
 // The unit of work is a warp with its whole piece in registers, and every global access is
-// 16 bytes per lane over contiguous rows.  No shared memory and no block-wide barrier:
-// the warps of an SM cover one another's latency.
+// 16 bytes per lane over contiguous rows.  No shared-memory staging: the warps of an SM cover
+// one another's latency.
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -97,10 +97,14 @@ __device__ __forceinline__ uint4 quantise16(const uint4 (&raw)[2], float* scale)
 // copy rate; 64 tokens take about 4 us, a launch and two round trips to memory.
 template <bool kInterleaved, bool kFp8>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p) {
+  // One warp does the block's double-precision work: with every warp doing it, 8000 tokens of
+  // one head took 8.1 us.
+  __shared__ uint64_t all_turns[32];
   const int lane = threadIdx.x & 31;
-  const float freq = p.inv_freq[lane];
-  const bool finite = fabsf(freq) < INFINITY;
-  const uint64_t turns = finite ? turns_of(freq) : 0;
+  const bool finite = fabsf(p.inv_freq[lane]) < INFINITY;
+  if (threadIdx.x < 32) all_turns[lane] = finite ? turns_of(p.inv_freq[lane]) : 0;
+  __syncthreads();
+  const uint64_t turns = all_turns[lane];
   const int axis = lane < p.section0 ? 0 : lane < p.section0 + p.section1 ? 1 : 2;
   const int units = (p.heads + kHeadsPerUnit - 1) / kHeadsPerUnit + 1;
   const long long total = (long long)p.tokens * units;

@@ -134,14 +134,15 @@ mla::PoolParams params_of(const mla_pool* pool, int n) {
   return p;
 }
 
-// Workspace: free-page bitmap, free pages before each of its words, claims, pages taken,
+// Workspace: free-page bitmap, free pages before each of its words and spans, claims, pages taken,
 // then the entries' decisions.
 struct PoolLayout {
-  size_t before, claim, pages, old_len, first, total;
+  size_t before, base, claim, pages, old_len, first, total;
   PoolLayout(const mla_pool* pool, int n) {
     const size_t words = ((size_t)pool->num_pages + 31) / 32;
     before = mla::align_up(words * 4, 256);
-    claim = before + mla::align_up(words * 4, 256);
+    base = before + mla::align_up(words * 4, 256);
+    claim = base + mla::align_up(words / 256 * 4 + 4, 256);
     pages = claim + mla::align_up((size_t)pool->max_rows * 4, 256);
     old_len = pages + mla::align_up((size_t)pool->num_pages * 4, 256);
     first = old_len + mla::align_up((size_t)n * 4, 256);
@@ -156,6 +157,7 @@ int work_of(const mla_pool* pool, int n, void* workspace, size_t bytes, mla::Poo
   auto* ws = static_cast<uint8_t*>(workspace);
   w->bits = reinterpret_cast<uint32_t*>(ws);
   w->before = reinterpret_cast<int32_t*>(ws + lay.before);
+  w->base = reinterpret_cast<int32_t*>(ws + lay.base);
   w->claim = reinterpret_cast<int32_t*>(ws + lay.claim);
   w->pages = reinterpret_cast<int32_t*>(ws + lay.pages);
   w->old_len = reinterpret_cast<int32_t*>(ws + lay.old_len);

@@ -9,12 +9,10 @@
 //
 // A call is two launches on one stream: one block that makes a bitmap of the free pages (one
 // pass over ref_count, 4 bytes a page), numbers them and decides every entry, and a grid that
-// applies the decisions.  For a pool of more than 65,536 pages a grid makes the bitmap first.
+// applies the decisions.  For a pool of more than 16,384 pages a grid makes the bitmap first.
 // Nothing but integers is computed; the counters that several threads change are changed by
 // integer atomics, whose order does not matter.  What bounds these calls is latency: the
-// plan is a chain of dependent loads (row, length, last page, its count) and block scans, about
-// 8 us with cold caches for 4096 pages and 16 us for 65,536; freeing takes 4 us, sharing or
-// adding blocks 4 to 6 us, a compaction's tables 6 to 7 us.
+// plan is a chain of dependent loads (row, length, last page, its count) and block scans.
 #include "launch.h"
 #include "mla_paged.h"
 
@@ -35,15 +33,46 @@ __device__ __forceinline__ int used_blocks(const PoolParams& p, int len) {
 
 __device__ __forceinline__ bool is_page(const PoolParams& p, int page) { return page >= 0 && page < p.num_pages; }
 
-// Bit i of word w: page 32 w + i is free.
-__global__ void __launch_bounds__(256) free_bitmap_kernel(PoolParams p, uint32_t* bits) {
-  const int words = (p.num_pages + 31) / 32;
-  const int lane = threadIdx.x & 31;
-  for (int w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < words; w += (gridDim.x * blockDim.x) >> 5) {
-    const int page = 32 * w + lane;
-    const unsigned b = __ballot_sync(0xffffffffu, page < p.num_pages && p.ref_count[page] <= 0);
-    if (lane == 0) bits[w] = b;
+// Bit i of word w: page 32 w + i is free; before[w]: free pages in the earlier words of the
+// word's span.  One block a span; totals[span] = its free pages.
+constexpr int kSpan = 256;
+
+__global__ void __launch_bounds__(kSpan) free_bitmap_kernel(PoolParams p, PoolWork w) {
+  __shared__ int warps[kSpan / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int words = (p.num_pages + 31) / 32, w0 = blockIdx.x * kSpan + 32 * warp;
+  int32_t ref[32];  // the counts of the warp's 32 words
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const long long page = 32LL * (w0 + k) + lane;
+    ref[k] = page < p.num_pages ? p.ref_count[page] : 1;
   }
+  uint32_t mine = 0;  // lane k keeps word w0 + k
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const unsigned b = __ballot_sync(0xffffffffu, ref[k] <= 0);
+    if (lane == k) mine = b;
+  }
+  const int c = __popc(mine);
+  int incl = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) warps[warp] = incl;
+  __syncthreads();
+  int at = incl - c, all = 0;
+#pragma unroll
+  for (int i = 0; i < kSpan / 32; ++i) {
+    if (i < warp) at += warps[i];
+    all += warps[i];
+  }
+  if (w0 + lane < words) {
+    w.bits[w0 + lane] = mine;
+    w.before[w0 + lane] = at;
+  }
+  if (threadIdx.x == 0) w.base[blockIdx.x] = all;
 }
 
 // Exclusive sum of v over the block; *total = the block's sum.
@@ -73,63 +102,96 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part, lo
   return before + incl - v;
 }
 
-// The free pages of a pool, as the plan's block sees them.  kNear: the block makes the bitmap
-// itself and keeps it in shared memory (with the pages before every word); otherwise both
-// are in the workspace.
+// The numbered free pages: base (nullptr: zeros) has the free pages before each span.
+struct FreeView {
+  const uint32_t* bits;
+  const int32_t* before;
+  const int32_t* base;
+  __device__ int before_word(int i) const { return before[i] + (base ? base[i / kSpan] : 0); }
+  __device__ int before_page(int page) const {
+    return before_word(page >> 5) + __popc(bits[page >> 5] & ((1u << (page & 31)) - 1u));
+  }
+  __device__ bool is_free(int page) const { return (bits[page >> 5] >> (page & 31)) & 1u; }
+  // The j-th free page (j < the number of free pages).
+  __device__ int page(int words, int j) const {
+    int lo = 0, hi = words - 1;  // last word with at most j free pages before it
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (before_word(mid) <= j) lo = mid; else hi = mid - 1;
+    }
+    uint32_t b = bits[lo];
+    for (int k = j - before_word(lo); k > 0; --k) b &= b - 1;
+    return 32 * lo + __ffs(b) - 1;
+  }
+};
+
+// The plan's numbering.  kNear: the block makes the bitmap itself, in shared memory;
+// otherwise the grid before it did, span by span, and the block adds up the spans.
+// Fork calls that need no page took (warm) 5.5 us for 4096 pages near; for 65,536 pages a
+// near bitmap took 12.7 us.
+constexpr int kNearWords = 512;
+
 template <bool kNear>
 struct FreePages {
   const PoolParams& p;
   const PoolWork& w;
-  uint32_t* bits;
-  int32_t* before;
-  __device__ FreePages(const PoolParams& pool, const PoolWork& work, uint32_t* near_bits, int32_t* near_before)
-      : p(pool), w(work), bits(kNear ? near_bits : work.bits), before(kNear ? near_before : work.before) {}
+  uint32_t* near_bits;
+  int32_t* near_before;
+  __device__ FreePages(const PoolParams& pool, const PoolWork& work, uint32_t* bits, int32_t* before)
+      : p(pool), w(work), near_bits(bits), near_before(before) {}
+  __device__ int words() const { return (p.num_pages + 31) / 32; }
+  __device__ FreeView view() const {
+    return kNear ? FreeView{near_bits, near_before, nullptr} : FreeView{w.bits, w.before, w.base};
+  }
 
   // Numbers the free pages and returns how many there are (called by the whole block).
   __device__ long long number(long long* part) {
-    const int words = (p.num_pages + 31) / 32;
+    long long run = 0, total;
     if constexpr (kNear) {
       const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-      constexpr int kFlight = 32;  // words of a warp in flight
-      for (int w0 = kFlight * warp; w0 < words; w0 += kFlight * (kPlanThreads / 32)) {
-        int32_t ref[kFlight];
+      constexpr int kFlight = kNearWords / (kPlanThreads / 32);  // words of a warp, all in flight
+      const int w0 = kFlight * warp;
+      int32_t ref[kFlight];
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-          const int page = 32 * (w0 + k) + lane;
-          ref[k] = page < p.num_pages ? p.ref_count[page] : 1;
-        }
-        uint32_t mine = 0;  // lane k keeps word w0 + k
-#pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-          const unsigned b = __ballot_sync(0xffffffffu, ref[k] <= 0);
-          if (lane == k) mine = b;
-        }
-        if (lane < kFlight && w0 + lane < words) bits[w0 + lane] = mine;
+      for (int k = 0; k < kFlight; ++k) {
+        const int page = 32 * (w0 + k) + lane;
+        ref[k] = page < p.num_pages ? p.ref_count[page] : 1;
       }
+      uint32_t mine = 0;  // lane k keeps word w0 + k
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const unsigned b = __ballot_sync(0xffffffffu, ref[k] <= 0);
+        if (lane == k) mine = b;
+      }
+      if (lane < kFlight) near_bits[w0 + lane] = mine;
       __syncthreads();
+      const int i = threadIdx.x;
+      const long long at = block_scan(i < kNearWords ? __popc(near_bits[i]) : 0, part, &run);
+      if (i < kNearWords) near_before[i] = (int32_t)at;
+    } else {
+      const int spans = (words() + kSpan - 1) / kSpan;
+      for (int base = 0; base < spans; base += kPlanThreads) {
+        const int i = base + threadIdx.x;
+        const long long at = run + block_scan(i < spans ? w.base[i] : 0, part, &total);
+        if (i < spans) w.base[i] = (int32_t)at;
+        run += total;
+      }
     }
-    long long run = 0, total;
-    for (int base = 0; base < words; base += kPlanThreads) {
-      const int i = base + threadIdx.x;
-      const long long c = i < words ? __popc(bits[i]) : 0;
-      const long long at = run + block_scan(c, part, &total);
-      if (i < words) before[i] = (int32_t)at;
-      run += total;
-    }
+    __syncthreads();
     return run;
   }
 
   // The ids of the first `need` free pages, in order.
   __device__ void list(long long need) {
-    const int words = (p.num_pages + 31) / 32;
-    for (int i = threadIdx.x; i < words; i += kPlanThreads) {
-      uint32_t b = bits[i];
-      for (long long r = before[i]; b && r < need; ++r, b &= b - 1) w.pages[r] = 32 * i + __ffs(b) - 1;
+    const FreeView v = view();
+    for (int base = 0; base < words() && v.before_word(base) < need; base += kPlanThreads) {
+      const int i = base + threadIdx.x;
+      if (i >= words()) break;
+      uint32_t b = v.bits[i];
+      for (long long r = v.before_word(i); b && r < need; ++r, b &= b - 1) w.pages[r] = 32 * i + __ffs(b) - 1;
     }
   }
 };
-
-constexpr int kNearWords = 2048;  // 65,536 pages: the plan's block reads their counts in about 2 us
 
 // One block: decides every entry in list order.  Entry i is valid if its indices are and no
 // earlier entry names its row; a valid entry is granted if it needs no page, or if the
@@ -302,43 +364,22 @@ __global__ void __launch_bounds__(kApplyThreads) free_kernel(PoolParams p) {
 
 // Compaction.  With L live pages, the live pages with ids >= L move, in order, to the free
 // pages with ids < L: as many of the one as of the other.
-__device__ __forceinline__ int free_before(const uint32_t* bits, const int32_t* before, int page) {
-  return before[page >> 5] + __popc(bits[page >> 5] & ((1u << (page & 31)) - 1u));
-}
-
-// The j-th free page (j < the number of free pages).
-__device__ __forceinline__ int free_page(const uint32_t* bits, const int32_t* before, int words, int j) {
-  int lo = 0, hi = words - 1;  // last word with at most j free pages before it
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (before[mid] <= j) lo = mid; else hi = mid - 1;
-  }
-  uint32_t b = bits[lo];
-  for (int k = j - before[lo]; k > 0; --k) b &= b - 1;
-  return 32 * lo + __ffs(b) - 1;
-}
-
 template <bool kNear>
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PoolParams p, PoolWork w) {
   __shared__ long long part[32];
   __shared__ uint32_t near_bits[kNear ? kNearWords : 1];
   __shared__ int32_t near_before[kNear ? kNearWords : 1];
-  __shared__ int moves;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   FreePages<kNear> free(p, w, near_bits, near_before);
   const int live = p.num_pages - (int)free.number(part);
-  if (threadIdx.x == 0) moves = 0;  // (no page is free: none moves)
-  __syncthreads();
-  const int words = (p.num_pages + 31) / 32;
   if constexpr (kNear)
-    for (int i = threadIdx.x; i < words; i += kPlanThreads) {
-      w.bits[i] = free.bits[i];
-      w.before[i] = free.before[i];
+    for (int i = threadIdx.x; i < free.words(); i += kPlanThreads) {
+      w.bits[i] = near_bits[i];
+      w.before[i] = near_before[i];
     }
   if (threadIdx.x == 0) {
-    if (live < p.num_pages) moves = free_before(free.bits, free.before, live);
     p.counts[0] = live;
-    p.counts[1] = moves;
+    p.counts[1] = live < p.num_pages ? free.view().before_page(live) : 0;  // no page is free: none moves
   }
 }
 
@@ -349,23 +390,19 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(PoolParams p, PoolWo
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the page copies)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int live = p.counts[0], moves = p.counts[1], words = (p.num_pages + 31) / 32;
-  const uint32_t* bits = w.bits;
-  const int32_t* before = w.before;
   if constexpr (kNear) {  // the searches below are chains of dependent reads
     for (int i = threadIdx.x; i < words; i += blockDim.x) {
       near_bits[i] = w.bits[i];
       near_before[i] = w.before[i];
     }
     __syncthreads();
-    bits = near_bits;
-    before = near_before;
   }
+  const FreeView v = kNear ? FreeView{near_bits, near_before, nullptr} : FreeView{w.bits, w.before, w.base};
   const long long tid = blockIdx.x * blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
-  auto is_free = [&](int page) { return (bits[page >> 5] >> (page & 31)) & 1u; };
-  auto move_of = [&](int page) { return page - free_before(bits, before, page) - (live - moves); };  // of a live page >= live
+  auto move_of = [&](int page) { return page - v.before_page(page) - (live - moves); };  // of a live page >= live
   for (long long page = live + tid; page < p.num_pages; page += step) {
-    if (is_free((int)page)) continue;
-    const int j = move_of((int)page), to = free_page(bits, before, words, j);
+    if (v.is_free((int)page)) continue;
+    const int j = move_of((int)page), to = v.page(words, j);
     p.src[j] = (int)page;
     p.dst[j] = to;
     p.ref_count[to] = p.ref_count[page];
@@ -377,8 +414,8 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(PoolParams p, PoolWo
     const int row = (int)(c / p.max_blocks), k = (int)(c - (long long)row * p.max_blocks);
     if (k >= blocks_of(p.seq_lens[row], p.page_size)) continue;
     const int page = p.block_table[c];
-    if (page < live || page >= p.num_pages || is_free(page)) continue;
-    p.block_table[c] = free_page(bits, before, words, move_of(page));
+    if (page < live || page >= p.num_pages || v.is_free(page)) continue;
+    p.block_table[c] = v.page(words, move_of(page));
   }
 }
 
@@ -392,7 +429,7 @@ bool near_pool(const PoolParams& p) { return p.num_pages <= 32 * kNearWords; }
 // The bitmap of a large pool.
 cudaError_t launch_bitmap(const PoolParams& p, const PoolWork& w, cudaStream_t stream) {
   if (near_pool(p)) return cudaSuccess;
-  free_bitmap_kernel<<<grid_of(p.num_pages, 256, 1216), 256, 0, stream>>>(p, w.bits);
+  free_bitmap_kernel<<<(p.num_pages - 1) / (32 * kSpan) + 1, kSpan, 0, stream>>>(p, w);
   return cudaGetLastError();
 }
 

@@ -136,6 +136,28 @@ def test_append_fp8_extreme_values(lib):
     assert torch.equal(got[:, 528:].contiguous().view(torch.bfloat16), kv[:, 512:])  # position 0: unchanged
 
 
+def test_append_fp8_every_magnitude(lib):
+    """Tiles of every bf16 exponent, values spread over 30 binades below their largest, zeros of
+    both signs: the bytes are those of the IEEE quotient."""
+    require_gpu()
+    g = torch.Generator().manual_seed(51)
+    kv = torch.randn(254 * 4, 576, generator=g)
+    spread = torch.randint(-30, 1, kv.shape, generator=g)
+    exponent = torch.arange(-126, 128).repeat_interleave(4)[:, None]
+    kv = torch.ldexp(kv.clamp(-1.9, 1.9), (spread + exponent).clamp(min=-140)).to(torch.bfloat16)
+    kv[:, 7], kv[:, 8] = 0.0, -0.0
+    assert torch.isfinite(kv).all()
+    n = kv.shape[0]
+    cache = torch.zeros(1, n, 656, dtype=torch.uint8).cuda()
+    d = kv.cuda()
+    lib.mla_rope_append_fp8(None, d[:, :512], d[:, 512:], torch.zeros(n, dtype=torch.int32).cuda(),
+                            torch.from_numpy(FREQ).cuda(), torch.arange(n, dtype=torch.int32).cuda(), cache)
+    codes, scales = co.quantise(kv[:, :512].float().numpy())
+    got = cache.cpu()[0]
+    assert torch.equal(got[:, 512:528].contiguous().view(torch.float32), torch.from_numpy(scales))
+    assert torch.equal(got[:, :512], torch.from_numpy(codes))
+
+
 @pytest.mark.parametrize("n", [0, 1, 3, 4, 5, 129, 5000])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_gather(lib, n, fp8):

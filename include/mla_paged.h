@@ -358,8 +358,9 @@ int mla_cache_copy_pages_fp8(void* kv_fp8, const int32_t* src, const int32_t* ds
  *   ref_count   [num_pages] int32: how many rows hold the page; 0 = free
  * A row's entries past its last page in use are neither read nor changed.  A new pool has
  * seq_lens and ref_count zero.  A caller may hold pages of its own (a prefix kept for later)
- * by adding to their ref_count.  The arrays are what mla_block_table_to_csr and
- * mla_paged_decode_block_table take.  The calls are deterministic: pages are taken lowest
+ * by adding to their ref_count.  A row's length changes through these calls only (a length
+ * lowered by hand would leave the pages behind it counted).  The arrays are what
+ * mla_block_table_to_csr and mla_paged_decode_block_table take.  The calls are deterministic: pages are taken lowest
  * id first in the order of the entries.
  *
  * mla_pages_extend: row rows[i] grows by new_tokens[i] >= 0 tokens.
@@ -444,8 +445,9 @@ int mla_read_device_status(void* workspace, void* stream);
  * Not thread-safe with respect to calls in flight on other threads. */
 int mla_debug_inject_timeout(int skip_tile, unsigned long long wait_ns);
 
-/* Kernel timing for benchmarks.  When enabled, every call records CUDA events on its
- * stream around its main attention kernel and its combine kernel;
+/* Kernel timing for benchmarks.  When enabled, every attention call records CUDA events on
+ * its stream around its main attention kernel (for the staged prefill: staging and
+ * attention) and its combine kernel;
  * mla_profile_read synchronises on the last events, returns the summed milliseconds
  * and the number of timed calls since the last read, and resets the sums. */
 int mla_profile_enable(int on);

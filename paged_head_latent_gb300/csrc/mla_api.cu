@@ -490,9 +490,16 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
     v.status = p.status;
     if (mla::launch_validate(v, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
   }
-  if (mla::launch_chunk_stage(p, fp8, stream) != cudaSuccess || mla::launch_chunk(maps, p, stream) != cudaSuccess ||
-      mla::launch_chunk_merge(p, stream) != cudaSuccess)
+  // Benchmark timing, as in run(): staging and attention, then the merge.
+  std::unique_lock<std::mutex> prof_lk(g_prof_mu);
+  cudaEvent_t* ev = profile_slot();
+  if (!ev) prof_lk.unlock();
+  if (ev) cudaEventRecord(ev[0], stream);
+  if (mla::launch_chunk_stage(p, fp8, stream) != cudaSuccess || mla::launch_chunk(maps, p, stream) != cudaSuccess)
     return MLA_ERR_LAUNCH;
+  if (ev) cudaEventRecord(ev[1], stream);
+  if (mla::launch_chunk_merge(p, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
+  if (ev) cudaEventRecord(ev[2], stream);
   return MLA_OK;
 }
 

@@ -258,7 +258,10 @@ int mla_noalloc_read_status(void* stream);
  * Causal prefill of a chunk of new tokens with staged keys: mla_paged_prefill's arguments,
  * mask and definition (the results differ in rounding).  The call first copies the keys it
  * needs into its workspace, so every page size and slot order runs at the same rate, and
- * attends in blocks of 128 (token, head) rows, so few heads cost no more than many.  Chunks
+ * attends in blocks of 128 (token, head) rows, so few heads cost no more than many: on four
+ * prompts with 128 heads and bf16 caches it takes half of mla_paged_prefill's time.  (For a
+ * token or a few per request over bf16 caches the decode calls, which read every key once,
+ * are faster.)  Chunks
  * may be ragged, down to one token or none per request; rows that see no key get out = 0,
  * lse = -inf.  dims->total_q may be larger than qo_indptr[batch], and num_kv_indices than
  * kv_indptr[batch]: the rows behind the last request are left as they were.  (MLA_VALIDATE

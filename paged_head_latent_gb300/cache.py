@@ -104,7 +104,7 @@ def _rope_append(name, q_pe, ckv, k_pe, positions, inv_freq, slots, cache, geome
     if ckv.shape != (tokens, HEAD_DIM_CKV) or k_pe.shape != (tokens, HEAD_DIM_KPE):
         raise ValueError("ckv must be [tokens, 512] and k_pe [tokens, 64]")
     _check("positions", positions, _I32, index)
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    axes = positions.shape[0] if positions.dim() == 2 else positions.dim()
     if positions.dim() > 2 or not 1 <= axes <= 3 or positions.shape[-1] != tokens:
         raise ValueError("positions must be [tokens] or [axes, tokens] with one to three axes")
     if sections is None:

@@ -6,7 +6,8 @@
 namespace mla {
 namespace {
 
-constexpr int kStageThreads = 512;
+constexpr int kStageThreads = 256;
+constexpr int kStageKeys = 32;  // keys of a staging block: one word of the tile's flags
 constexpr int kNear = 1024;  // entries of the plan's tables that are kept in shared memory too
 // Cost units (tiles) of starting a block: its Q load and its output.  Four prompts with 128 heads
 // took 935, 881, 871 and 886 us at 1 to 4, 32 blocks of drafted tokens 24.7, 22.9, 22.7 and 23.9.
@@ -132,14 +133,14 @@ __device__ void plan(const ChunkParams& p) {
   }
 }
 
-// One block per staged tile (and one more for the plan): 128 keys of one request, read
+// Four blocks per staged tile (and one more for the plan), 32 keys of one request each, read
 // through their slots, as the bf16 numbers that the cache holds or (kFp8) stands for.  Rows past
 // the request's keys, slots outside the cache and keys with a value that is not finite
 // are written as zeros, so that a weight of zero always makes a zero product; the tile's
-// flags tell which rows are keys and which of them were not finite.  Up to 1 % of a long
-// chunk's time (10 us for 9.4K keys); for 16K keys of short requests 8 us, four dependent
-// round trips (offsets, slots, tokens, the store) and the launch, with all of a warp's tokens
-// in flight at once.
+// flags tell which rows are keys and which of them were not finite.  301K FP8 keys (545 MB) take
+// 91 us, 6.0 TB/s (with one block of 128 keys a tile 115 us: one block an SM, nothing to cover its
+// waits); 16K keys of short requests 7 us, four dependent round trips (offsets, slots, tokens,
+// the store) and the launch.  The plan of 2059 blocks takes about 13 us beside it.
 template <bool kFp8>
 __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -147,9 +148,10 @@ __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkP
     plan(p);
     return;
   }
-  __shared__ uint32_t flags[8];
+  __shared__ uint32_t is_key, is_odd;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tile = blockIdx.x - 1;
+  constexpr int kParts = kChunkKeys / kStageKeys;
+  const int tile = (blockIdx.x - 1) / kParts, first = (blockIdx.x - 1) % kParts * kStageKeys;
   // The request: the last one whose first tile is <= tile (32 probes at a time).
   int lo = 0, n = p.batch;
   while (n > 1) {
@@ -167,11 +169,11 @@ __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkP
   const int here = min(kChunkKeys, r.kv_len - key0);
   // (a request without keys has one tile of zeros: its rows' weights are zero)
   if ((here <= 0 && key0 != 0) || key0 < 0 || r.q_len == 0) return;
-  constexpr int kTok = kChunkKeys * 32 / kStageThreads;  // a warp's tokens, all in flight
-  const int k0 = warp * kTok;
+  constexpr int kTok = kStageKeys * 32 / kStageThreads;  // a warp's tokens, all in flight
+  const int k0 = first + warp * kTok;
   int mine = -1;
   if (lane < kTok && k0 + lane < here) mine = __ldg(p.kv_indices + r.k0 + key0 + k0 + lane);
-  if (threadIdx.x < 8) flags[threadIdx.x] = 0;
+  if (threadIdx.x == 0) is_key = is_odd = 0;
   __syncthreads();
   if (mine >= p.num_slots) mine = -1;
   uint4 lat[kTok][kFp8 ? 1 : 2], rope[kTok];  // lane: latent values 16 lane .. + 15, rope values 8 lane .. + 7
@@ -215,12 +217,15 @@ __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkP
     dst[0] = a;
     dst[1] = b;
     if (lane < 8) *reinterpret_cast<uint4*>(p.kpe + row * kDimKpe + 8 * lane) = rope[k];
-    if (lane == 0 && bad) atomicOr(&flags[4 + ((k0 + k) >> 5)], 1u << ((k0 + k) & 31));
+    if (lane == 0 && bad) atomicOr(&is_odd, 1u << ((k0 + k) & 31));
   }
   const unsigned keys = __ballot_sync(0xffffffffu, mine >= 0);
-  if (lane == 0 && keys) atomicOr(&flags[k0 >> 5], keys << (k0 & 31));
+  if (lane == 0 && keys) atomicOr(&is_key, keys << (k0 & 31));
   __syncthreads();
-  if (threadIdx.x < 8) p.flags[(size_t)tile * 8 + threadIdx.x] = flags[threadIdx.x];
+  if (threadIdx.x == 0) {
+    p.flags[(size_t)tile * 8 + first / 32] = is_key;
+    p.flags[(size_t)tile * 8 + 4 + first / 32] = is_odd;
+  }
 }
 
 // Merge of split blocks.  Block (w, y): of the split block that worker w ends, if any, rows
@@ -295,8 +300,9 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
 }  // namespace
 
 cudaError_t launch_chunk_stage(const ChunkParams& p, bool fp8, cudaStream_t stream) {
-  if (fp8) chunk_stage_kernel<true><<<p.tiles + 1, kStageThreads, 0, stream>>>(p);
-  else chunk_stage_kernel<false><<<p.tiles + 1, kStageThreads, 0, stream>>>(p);
+  const int grid = p.tiles * (kChunkKeys / kStageKeys) + 1;  // (tiles * 128 is below 2^31)
+  if (fp8) chunk_stage_kernel<true><<<grid, kStageThreads, 0, stream>>>(p);
+  else chunk_stage_kernel<false><<<grid, kStageThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -126,9 +126,9 @@ struct FreeView {
 };
 
 // The plan's numbering.  kNear: the block makes the bitmap itself, in shared memory;
-// otherwise the grid before it did, span by span, and the block adds up the spans.
-// Fork calls that need no page took (warm) 5.5 us for 4096 pages near; for 65,536 pages a
-// near bitmap took 12.7 us.
+// otherwise the grid before it did, span by span, and the block adds up the spans.  A fork
+// that is refused takes (warm) 5.0 us near and 7.2 by the grid for 4096 pages, 5.2 and 6.9 for
+// 16,384; for 65,536 pages a bitmap of the block's own took 12.7 us, the grid's 7.0.
 constexpr int kNearWords = 512;
 
 template <bool kNear>

@@ -351,7 +351,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int local = it.blk.local0 + 64 * rank + r;  // row within its request
       if (first) seen = it.blk.seen + local / p.heads;
       const uint32_t* fl = p.flags + (size_t)(it.blk.tile0 + it.t) * 8 + quarter;
-      const uint32_t keys = __ldg(fl), odd = __ldg(fl + 4);
+      // (from L2: this kernel may have begun before the staging pass wrote them)
+      const uint32_t keys = __ldcg(fl), odd = __ldcg(fl + 4);
       if (!wait(S_FULL + (j & 1), (j >> 1) & 1)) {
         ok = false;
         break;

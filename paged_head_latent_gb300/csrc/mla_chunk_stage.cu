@@ -236,11 +236,13 @@ __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkP
 // to two long chunks (40 MB of fragments); a row to a warp, with the same reads 16 bytes at a
 // time, added 13 and 17.
 constexpr int kMergeThreads = 256, kMergeParts = 16;
+static_assert(sizeof(ChunkMerge) == 16, "read as one word");
 
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p) {
   const int w = blockIdx.x;
   // (the plan is older than the attention kernel, whose end the wait is for)
-  const ChunkMerge blk = p.merges[w];
+  const int4 plan = __ldcg(reinterpret_cast<const int4*>(p.merges + w));
+  const ChunkMerge blk{plan.x, plan.y, plan.z, plan.w};
   const int row = 32 * (blockIdx.y >> 2) + (threadIdx.x & 31);
   const int col = 128 * (blockIdx.y & 3) + 16 * (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;" ::: "memory");

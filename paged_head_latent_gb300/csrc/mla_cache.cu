@@ -325,10 +325,10 @@ cudaError_t launch_rope_append(const RopeParams& p, bool fp8, cudaStream_t strea
 }
 
 cudaError_t launch_gather(const GatherParams& p, bool fp8, cudaStream_t stream) {
-  // A warp's tokens are one pass of its block: blocks that end and begin at different times keep
-  // reads and writes mixed.
+  // A warp's tokens are one pass of its block (up to 311K tokens): blocks that end and begin at
+  // different times keep reads and writes mixed.
   constexpr int kTok = 4;
-  const int grid = blocks_for(((long long)p.n + kTok - 1) / kTok, 1 << 30);
+  const int grid = blocks_for(((long long)p.n + kTok - 1) / kTok, 152 * 64);
   if (fp8) gather_kernel<true, kTok><<<grid, kThreads, 0, stream>>>(p);
   else gather_kernel<false, kTok><<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();

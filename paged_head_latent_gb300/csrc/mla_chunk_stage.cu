@@ -133,14 +133,15 @@ __device__ void plan(const ChunkParams& p) {
   }
 }
 
-// Four blocks per staged tile (and one more for the plan), 32 keys of one request each, read
+// Block 0 makes the plan.  The others take parts of staged tiles: 32 keys of one request, read
 // through their slots, as the bf16 numbers that the cache holds or (kFp8) stands for.  Rows past
 // the request's keys, slots outside the cache and keys with a value that is not finite
 // are written as zeros, so that a weight of zero always makes a zero product; the tile's
 // flags tell which rows are keys and which of them were not finite.  301K FP8 keys (545 MB) take
-// 91 us, 6.0 TB/s (with one block of 128 keys a tile 115 us: one block an SM, nothing to cover its
+// 95 us, 5.7 TB/s (with one block of 128 keys a tile 115 us: one block an SM, nothing to cover its
 // waits); 16K keys of short requests 7 us, four dependent round trips (offsets, slots, tokens,
-// the store) and the launch.  The plan of 2059 blocks takes about 13 us beside it.
+// the store) and the launch; a buffer of 524K indices for 32K keys costs 1 us more.  The plan of
+// 2059 blocks takes about 13 us beside it.
 template <bool kFp8>
 __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -151,80 +152,86 @@ __global__ void __launch_bounds__(kStageThreads) chunk_stage_kernel(const ChunkP
   __shared__ uint32_t is_key, is_odd;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kParts = kChunkKeys / kStageKeys;
-  const int tile = (blockIdx.x - 1) / kParts, first = (blockIdx.x - 1) % kParts * kStageKeys;
-  // The request: the last one whose first tile is <= tile (32 probes at a time).
-  int lo = 0, n = p.batch;
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int b = lo + lane * step;
-    const bool below = lane * step < n &&
-        (min(max(__ldg(p.kv_indptr + b), 0), p.num_kv_indices) + kChunkKeys - 1) / kChunkKeys + b <= tile;
-    const int k = __popc(__ballot_sync(0xffffffffu, below));
-    const int at = max(k - 1, 0) * step;
-    lo += at;
-    n = min(step, n - at);
-  }
-  const ChunkReq r = load_request(p, lo);
-  const int key0 = (tile - r.tile0) * kChunkKeys;
-  const int here = min(kChunkKeys, r.kv_len - key0);
-  // (a request without keys has one tile of zeros: its rows' weights are zero)
-  if ((here <= 0 && key0 != 0) || key0 < 0 || r.q_len == 0) return;
-  constexpr int kTok = kStageKeys * 32 / kStageThreads;  // a warp's tokens, all in flight
-  const int k0 = first + warp * kTok;
-  int mine = -1;
-  if (lane < kTok && k0 + lane < here) mine = __ldg(p.kv_indices + r.k0 + key0 + k0 + lane);
-  if (threadIdx.x == 0) is_key = is_odd = 0;
-  __syncthreads();
-  if (mine >= p.num_slots) mine = -1;
-  uint4 lat[kTok][kFp8 ? 1 : 2], rope[kTok];  // lane: latent values 16 lane .. + 15, rope values 8 lane .. + 7
-  float sc[kTok];
-#pragma unroll
-  for (int k = 0; k < kTok; ++k) {
-    const int slot = __shfl_sync(0xffffffffu, mine, k);
-    lat[k][0] = lat[k][kFp8 ? 0 : 1] = rope[k] = make_uint4(0, 0, 0, 0);
-    sc[k] = 0.f;
-    if (slot < 0) continue;
-    if constexpr (kFp8) {
-      const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
-      lat[k][0] = *reinterpret_cast<const uint4*>(tok + 16 * lane);
-      sc[k] = *reinterpret_cast<const float*>(tok + kDimCkv + 4 * (lane >> 3));
-      if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
-    } else {
-      const uint4* tok = reinterpret_cast<const uint4*>(p.ckv_cache + (size_t)slot * kDimCkv + 16 * lane);
-      lat[k][0] = tok[0];
-      lat[k][1] = tok[1];
-      if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * lane);
+  // The list of keys may be shorter than its buffer: only the tiles in use are walked.
+  const int used = min(max(__ldg(p.kv_indptr + p.batch), 0), p.num_kv_indices);
+  const int parts = min(p.tiles, (used + kChunkKeys - 1) / kChunkKeys + p.batch) * kParts;
+  for (int at_part = blockIdx.x - 1; at_part < parts; at_part += gridDim.x - 1) {
+    const int tile = at_part / kParts, first = at_part % kParts * kStageKeys;
+    // The request: the last one whose first tile is <= tile (32 probes at a time).
+    int lo = 0, n = p.batch;
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const int b = lo + lane * step;
+      const bool below = lane * step < n &&
+          (min(max(__ldg(p.kv_indptr + b), 0), p.num_kv_indices) + kChunkKeys - 1) / kChunkKeys + b <= tile;
+      const int k = __popc(__ballot_sync(0xffffffffu, below));
+      const int at = max(k - 1, 0) * step;
+      lo += at;
+      n = min(step, n - at);
     }
-  }
+    const ChunkReq r = load_request(p, lo);
+    const int key0 = (tile - r.tile0) * kChunkKeys;
+    const int here = min(kChunkKeys, r.kv_len - key0);
+    // (a request without keys has one tile of zeros: its rows' weights are zero)
+    if ((here <= 0 && key0 != 0) || key0 < 0 || r.q_len == 0) continue;
+    constexpr int kTok = kStageKeys * 32 / kStageThreads;  // a warp's tokens, all in flight
+    const int k0 = first + warp * kTok;
+    int mine = -1;
+    if (lane < kTok && k0 + lane < here) mine = __ldg(p.kv_indices + r.k0 + key0 + k0 + lane);
+    __syncthreads();  // (the flags of the last round are written)
+    if (threadIdx.x == 0) is_key = is_odd = 0;
+    __syncthreads();
+    if (mine >= p.num_slots) mine = -1;
+    uint4 lat[kTok][kFp8 ? 1 : 2], rope[kTok];  // lane: latent values 16 lane .. + 15, rope values 8 lane .. + 7
+    float sc[kTok];
 #pragma unroll
-  for (int k = 0; k < kTok; ++k) {
-    uint4 a, b;
-    if constexpr (kFp8) {
-      a = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(lat[k][0].x, lat[k][0].y), sc[k]);
-      b = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(lat[k][0].z, lat[k][0].w), sc[k]);
-    } else {
-      a = lat[k][0];
-      b = lat[k][1];
+    for (int k = 0; k < kTok; ++k) {
+      const int slot = __shfl_sync(0xffffffffu, mine, k);
+      lat[k][0] = lat[k][kFp8 ? 0 : 1] = rope[k] = make_uint4(0, 0, 0, 0);
+      sc[k] = 0.f;
+      if (slot < 0) continue;
+      if constexpr (kFp8) {
+        const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
+        lat[k][0] = *reinterpret_cast<const uint4*>(tok + 16 * lane);
+        sc[k] = *reinterpret_cast<const float*>(tok + kDimCkv + 4 * (lane >> 3));
+        if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
+      } else {
+        const uint4* tok = reinterpret_cast<const uint4*>(p.ckv_cache + (size_t)slot * kDimCkv + 16 * lane);
+        lat[k][0] = tok[0];
+        lat[k][1] = tok[1];
+        if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * lane);
+      }
     }
-    const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, rope[k].x, rope[k].y, rope[k].z, rope[k].w};
-    uint32_t odd = 0;
 #pragma unroll
-    for (int i = 0; i < 12; ++i) odd |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);  // exponent all ones
-    const bool bad = __any_sync(0xffffffffu, odd != 0);
-    if (bad) a = b = rope[k] = make_uint4(0, 0, 0, 0);
-    const size_t row = (size_t)tile * kChunkKeys + k0 + k;
-    uint4* dst = reinterpret_cast<uint4*>(p.ckv + row * kDimCkv + 16 * lane);
-    dst[0] = a;
-    dst[1] = b;
-    if (lane < 8) *reinterpret_cast<uint4*>(p.kpe + row * kDimKpe + 8 * lane) = rope[k];
-    if (lane == 0 && bad) atomicOr(&is_odd, 1u << ((k0 + k) & 31));
-  }
-  const unsigned keys = __ballot_sync(0xffffffffu, mine >= 0);
-  if (lane == 0 && keys) atomicOr(&is_key, keys << (k0 & 31));
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    p.flags[(size_t)tile * 8 + first / 32] = is_key;
-    p.flags[(size_t)tile * 8 + 4 + first / 32] = is_odd;
+    for (int k = 0; k < kTok; ++k) {
+      uint4 a, b;
+      if constexpr (kFp8) {
+        a = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(lat[k][0].x, lat[k][0].y), sc[k]);
+        b = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(lat[k][0].z, lat[k][0].w), sc[k]);
+      } else {
+        a = lat[k][0];
+        b = lat[k][1];
+      }
+      const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, rope[k].x, rope[k].y, rope[k].z, rope[k].w};
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < 12; ++i) odd |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);  // exponent all ones
+      const bool bad = __any_sync(0xffffffffu, odd != 0);
+      if (bad) a = b = rope[k] = make_uint4(0, 0, 0, 0);
+      const size_t row = (size_t)tile * kChunkKeys + k0 + k;
+      uint4* dst = reinterpret_cast<uint4*>(p.ckv + row * kDimCkv + 16 * lane);
+      dst[0] = a;
+      dst[1] = b;
+      if (lane < 8) *reinterpret_cast<uint4*>(p.kpe + row * kDimKpe + 8 * lane) = rope[k];
+      if (lane == 0 && bad) atomicOr(&is_odd, 1u << ((k0 + k) & 31));
+    }
+    const unsigned keys = __ballot_sync(0xffffffffu, mine >= 0);
+    if (lane == 0 && keys) atomicOr(&is_key, keys << (k0 & 31));
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      p.flags[(size_t)tile * 8 + first / 32] = is_key;
+      p.flags[(size_t)tile * 8 + 4 + first / 32] = is_odd;
+    }
   }
 }
 
@@ -302,7 +309,8 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
 }  // namespace
 
 cudaError_t launch_chunk_stage(const ChunkParams& p, bool fp8, cudaStream_t stream) {
-  const int grid = p.tiles * (kChunkKeys / kStageKeys) + 1;  // (tiles * 128 is below 2^31)
+  const int parts = p.tiles * (kChunkKeys / kStageKeys);  // (tiles * 128 is below 2^31)
+  const int grid = 1 + (parts < 152 * 32 ? parts : 152 * 32);
   if (fp8) chunk_stage_kernel<true><<<grid, kStageThreads, 0, stream>>>(p);
   else chunk_stage_kernel<false><<<grid, kStageThreads, 0, stream>>>(p);
   return cudaGetLastError();

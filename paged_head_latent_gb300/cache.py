@@ -2,7 +2,8 @@
 
 Argument checks and marshalling only, like the package's other calls (include/mla_paged.h
 has the definitions).  Every tensor is on one CUDA device, the call runs there on ``stream``
-(default: that device's current stream), and nothing synchronises.
+(default: that device's current stream), and nothing synchronises.  What a call allocates
+(outputs and a workspace that are not given) belongs to that stream too.
 """
 
 from __future__ import annotations
@@ -76,23 +77,29 @@ def _ints(name, t, shape, index):
         raise ValueError(f"{name} must be {list(shape)} int32, got {list(t.shape)}")
 
 
-def _buffer(name, t, shape, dtype, like):
+def _new(make, shape, dtype, like, stream):
+    """A new tensor on the device of ``like``.  It belongs to the stream that the call runs on:
+    memory of another one could still be in use there, or be zeroed too late."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
+
+
+def _buffer(name, t, shape, dtype, like, stream):
     """``t``, checked, or a new tensor on the device of ``like``."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _new(torch.empty, shape, dtype, like, stream)
     _check(name, t, dtype, like.get_device())
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 
 
-def _scratch(workspace, need, like, what):
-    if workspace is None:
-        if need == 0:
-            raise MlaError(-2, what)
-        return torch.zeros(need, dtype=_U8, device=like.device)
-    _check("workspace", workspace, _U8, like.get_device())
-    return workspace
+def _scratch(make, need, like, stream, what):
+    if need == 0:
+        raise MlaError(-2, what)
+    return _new(make, need, _U8, like, stream)
 
 
 # ---------------------------------------------------------------- rotary positions and the cache write
@@ -130,7 +137,7 @@ def _rope_append(name, q_pe, ckv, k_pe, positions, inv_freq, slots, cache, geome
         q_token, q_head, last = q_pe.stride()
         if last != 1 and tokens and heads:
             raise ValueError("the last dimension of q_pe must be contiguous")
-        q_out = _buffer("q_out", q_out, (tokens, heads, HEAD_DIM_KPE), _BF16, q_pe)
+        q_out = _buffer("q_out", q_out, (tokens, heads, HEAD_DIM_KPE), _BF16, q_pe, stream)
     ckv_row, ckv_last = ckv.stride()
     kpe_row, kpe_last = k_pe.stride()
     if (ckv_last != 1 or kpe_last != 1) and tokens:
@@ -180,8 +187,8 @@ def _gather(name, cache, like, geometry, slots, ckv_out, kpe_out, count, stream)
     if slots.dim() != 1:
         raise ValueError("slots must be [n]")
     n = slots.shape[0]
-    ckv_out = _buffer("ckv_out", ckv_out, (n, HEAD_DIM_CKV), _BF16, like)
-    kpe_out = _buffer("kpe_out", kpe_out, (n, HEAD_DIM_KPE), _BF16, like)
+    ckv_out = _buffer("ckv_out", ckv_out, (n, HEAD_DIM_CKV), _BF16, like, stream)
+    kpe_out = _buffer("kpe_out", kpe_out, (n, HEAD_DIM_KPE), _BF16, like, stream)
     _call(name, index, stream, *cache, slots.data_ptr(), n, None if count is None else _count(count, index),
           geometry[0], geometry[1], ckv_out.data_ptr(), kpe_out.data_ptr())
     return ckv_out, kpe_out
@@ -257,17 +264,17 @@ def _prefill(name, q_nope, q_pe, cache, geometry, qo_indptr, kv_indptr, kv_indic
     if batch < 0 or qo_indptr.numel() != batch + 1:
         raise ValueError("qo_indptr and kv_indptr must both have batch + 1 entries")
     dims = make_dims(batch, heads, geometry[0], geometry[1], kv_indices.numel(), total_q=rows, num_workers=num_workers)
-    out = _buffer("out", out, (rows, heads, HEAD_DIM_CKV), _BF16, q_nope)
-    lse = _buffer("lse", lse, (rows, heads), _F32, q_nope)
+    out = _buffer("out", out, (rows, heads, HEAD_DIM_CKV), _BF16, q_nope, stream)
+    lse = _buffer("lse", lse, (rows, heads), _F32, q_nope, stream)
     if workspace is None:
         with torch.cuda.device(index):
             need = workspace_bytes_prefill_staged(dims)
-        workspace = _scratch(None, need, q_nope, "mla_workspace_bytes_prefill_staged")
+        workspace = _scratch(torch.zeros, need, q_nope, stream, "mla_workspace_bytes_prefill_staged")
     else:  # (the library checks its size)
         _check("workspace", workspace, _U8, index)
     _call(name, index, stream, q_nope.data_ptr(), q_pe.data_ptr(), *cache, qo_indptr.data_ptr(), kv_indptr.data_ptr(),
-          kv_indices.data_ptr(), sm_scale, out.data_ptr(), lse.data_ptr(), ctypes.byref(dims), workspace.data_ptr(),
-          workspace.numel(), flags)
+          kv_indices.data_ptr(), float(sm_scale), out.data_ptr(), lse.data_ptr(), ctypes.byref(dims), workspace.data_ptr(),
+          workspace.numel(), int(flags))
     return out, lse
 
 
@@ -323,11 +330,11 @@ def _entries(name, t, index):
     return t.shape[0]
 
 
-def _pool_scratch(workspace, pool, n, like):
+def _pool_scratch(workspace, pool, n, like, stream):
     if workspace is not None:  # (the library checks its size)
         _check("workspace", workspace, _U8, like.get_device())
         return workspace
-    return _scratch(None, int(lib().mla_workspace_bytes_pages(ctypes.byref(pool), n)), like,
+    return _scratch(torch.empty, int(lib().mla_workspace_bytes_pages(ctypes.byref(pool), n)), like, stream,
                     "mla_workspace_bytes_pages")
 
 
@@ -343,10 +350,10 @@ def mla_pages_extend(block_table, seq_lens, ref_count, rows, new_tokens, page_si
     capacity = int(capacity)
     if capacity < 0:
         raise ValueError("capacity must not be negative")
-    new_indptr = _buffer("new_indptr", new_indptr, (n + 1,), _I32, block_table)
-    slots = _buffer("slots", slots, (capacity,), _I32, block_table)
-    results = _buffer("results", results, (n,), _I32, block_table)
-    workspace = _pool_scratch(workspace, pool, n, block_table)
+    new_indptr = _buffer("new_indptr", new_indptr, (n + 1,), _I32, block_table, stream)
+    slots = _buffer("slots", slots, (capacity,), _I32, block_table, stream)
+    results = _buffer("results", results, (n,), _I32, block_table, stream)
+    workspace = _pool_scratch(workspace, pool, n, block_table, stream)
     _call("mla_pages_extend", index, stream, ctypes.byref(pool), rows.data_ptr(), new_tokens.data_ptr(), n,
           new_indptr.data_ptr(), slots.data_ptr(), capacity, results.data_ptr(), workspace.data_ptr(),
           workspace.numel())
@@ -361,11 +368,11 @@ def mla_pages_fork(block_table, seq_lens, ref_count, parents, children, page_siz
     pool, index = _pool(block_table, seq_lens, ref_count, page_size)
     n = _entries("parents", parents, index)
     _ints("children", children, (n,), index)
-    results = _buffer("results", results, (n,), _I32, block_table)
-    src = _buffer("src", src, (n,), _I32, block_table)
-    dst = _buffer("dst", dst, (n,), _I32, block_table)
-    copy_tokens = _buffer("copy_tokens", copy_tokens, (n,), _I32, block_table)
-    workspace = _pool_scratch(workspace, pool, n, block_table)
+    results = _buffer("results", results, (n,), _I32, block_table, stream)
+    src = _buffer("src", src, (n,), _I32, block_table, stream)
+    dst = _buffer("dst", dst, (n,), _I32, block_table, stream)
+    copy_tokens = _buffer("copy_tokens", copy_tokens, (n,), _I32, block_table, stream)
+    workspace = _pool_scratch(workspace, pool, n, block_table, stream)
     _call("mla_pages_fork", index, stream, ctypes.byref(pool), parents.data_ptr(), children.data_ptr(), n,
           src.data_ptr(), dst.data_ptr(), copy_tokens.data_ptr(), results.data_ptr(), workspace.data_ptr(),
           workspace.numel())
@@ -386,10 +393,10 @@ def mla_pages_compact(block_table, seq_lens, ref_count, page_size, counts=None, 
     count=counts[1:])`` for every cache."""
     pool, index = _pool(block_table, seq_lens, ref_count, page_size)
     moves = ref_count.shape[0] // 2
-    counts = _buffer("counts", counts, (2,), _I32, block_table)
-    src = _buffer("src", src, (moves,), _I32, block_table)
-    dst = _buffer("dst", dst, (moves,), _I32, block_table)
-    workspace = _pool_scratch(workspace, pool, 0, block_table)
+    counts = _buffer("counts", counts, (2,), _I32, block_table, stream)
+    src = _buffer("src", src, (moves,), _I32, block_table, stream)
+    dst = _buffer("dst", dst, (moves,), _I32, block_table, stream)
+    workspace = _pool_scratch(workspace, pool, 0, block_table, stream)
     _call("mla_pages_compact", index, stream, ctypes.byref(pool), counts.data_ptr(), src.data_ptr(), dst.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return counts, src, dst

@@ -424,3 +424,44 @@ def test_serving_steps_end_to_end(lib):
     for r in (2, 3, 4, 5):
         n = kept[r][0].shape[0]
         assert torch.equal(seen[r][0][:n], kept[r][0]) and torch.equal(seen[r][1][:n], kept[r][1])
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(lib):
+    """Freed memory of the current stream, with a write still to come, is not what a call on
+    another stream returns: outputs on a side stream keep what the call wrote."""
+    require_gpu()
+    x = make([60, 9], [500, 130], 16, 64, seed=44)
+    ref = plain(x)
+    c = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    slots = torch.arange(500, dtype=torch.int32, device="cuda")
+    table = torch.full((4, 2000), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(4, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(8000, dtype=torch.int32, device="cuda")
+    rows = torch.arange(4, dtype=torch.int32, device="cuda")
+    new = torch.full((4,), 2000, dtype=torch.int32, device="cuda")
+    latent = torch.randn(69, 512, device="cuda").to(torch.bfloat16)
+    key = torch.randn(69, 64, device="cuda").to(torch.bfloat16)
+    pos = torch.zeros(69, dtype=torch.int32, device="cuda")
+    freq = torch.ones(32, device="cuda")
+    nowhere = torch.full((69,), -1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    rows_ref = lib.mla_cache_gather_fp8(c["kv"], slots)
+
+    def calls(stream):
+        return (lib.mla_paged_prefill_fp8(c["qn"], c["qp"], c["kv"], c["qo"], c["kp"], c["ki"], c["scale"], stream=stream),
+                lib.mla_cache_gather_fp8(c["kv"], slots, stream=stream),
+                lib.mla_pages_extend(table, lens, refs, rows, new, 1, 8000, stream=stream),
+                lib.mla_rope_append_fp8(c["qp"], latent, key, pos, freq, nowhere, c["kv"], stream=stream))
+
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    sizes = (69 * 16 * 512 * 2, 69 * 16 * 4, 500 * 512 * 2, 500 * 64 * 2, 8000 * 4, 20, 16, 69 * 16 * 64 * 2)
+    late = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    del late  # (their memory is free for this stream, their writes are still to come)
+    got, gathered, (indptr, taken, results), rotated = calls(side)
+    torch.cuda.synchronize()
+    close(got, ref)
+    assert all(torch.equal(a, b) for a, b in zip(gathered, rows_ref))
+    assert results.tolist() == [0] * 4 and indptr.tolist() == [0, 2000, 4000, 6000, 8000]
+    assert torch.equal(taken.cpu(), torch.arange(8000, dtype=torch.int32))
+    assert torch.equal(rotated, c["qp"])

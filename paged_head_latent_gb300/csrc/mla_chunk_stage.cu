@@ -68,14 +68,15 @@ __device__ void plan(const ChunkParams& p) {
     const int b = base + threadIdx.x;
     long long n = 0;
     if (b < p.batch) n = ((long long)load_request(p, b).q_len * p.heads + kChunkRows - 1) / kChunkRows;
-    const int at = (int)(run + scan(n, &total));
+    const int at = (int)min(run + scan(n, &total), 0x7fffffffLL);  // (overlapping offsets: see nblocks)
     if (b < p.batch) {
       if (b < kNear) near_first[b] = at;
       else p.first_block[b] = at;
     }
     run += total;
   }
-  const int nblocks = (int)min(run, (long long)p.max_blocks);  // (offsets that overlap could name more)
+  // Offsets that overlap could name more blocks than there is room for, even more than an int holds.
+  const int nblocks = (int)min(run, (long long)p.max_blocks);
   __syncthreads();
   long long cost = 0;
   for (int base = 0; base < nblocks; base += kStageThreads) {

@@ -369,7 +369,7 @@ int mla_cache_copy_pages_fp8(void* kv_fp8, const int32_t* src, const int32_t* ds
  * mla_pages_extend: row rows[i] grows by new_tokens[i] >= 0 tokens.
  *   results [n]: MLA_OK; MLA_ERR_BAD_INDEX (nothing changes) if the row is out of range or
  *     named by an earlier entry, the count negative, the new length over max_blocks *
- *     page_size, or the row's last, partly filled page shared with another row;
+ *     page_size, or the row's last, partly filled page held by anyone else too;
  *     MLA_ERR_NO_PAGES (nothing changes) if the entry needs pages and the free pages do not
  *     cover it together with all earlier valid entries
  *   new_indptr [n + 1]: offsets of the granted tokens (refused entries add none), packed in

@@ -19,6 +19,11 @@ bool cache_dims(int num_pages, int page_size) {
 
 int launched(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_LAUNCH; }
 
+cudaStream_t stream_of(void* stream) {
+  cudaGetLastError();  // clear stale errors so the checks after the launches see only ours
+  return static_cast<cudaStream_t>(stream);
+}
+
 int rope_append(const void* q_pe, const void* ckv, const void* k_pe, const int32_t* positions, const float* inv_freq,
                 const int32_t* slots, void* q_out, void* ckv_cache, void* kpe_cache, void* kv_fp8, bool fp8,
                 const mla_rope_dims* d, void* stream) {
@@ -62,7 +67,7 @@ int rope_append(const void* q_pe, const void* ckv, const void* k_pe, const int32
   p.section0 = d->section[0];
   p.section1 = d->num_axes > 1 ? d->section[1] : 0;
   p.interleaved = d->interleaved != 0;
-  return launched(mla::launch_rope_append(p, fp8, static_cast<cudaStream_t>(stream)));
+  return launched(mla::launch_rope_append(p, fp8, stream_of(stream)));
 }
 
 int gather(const void* ckv, const void* kpe, const void* kv_fp8, bool fp8, const int32_t* slots, int n,
@@ -83,7 +88,7 @@ int gather(const void* ckv, const void* kpe, const void* kv_fp8, bool fp8, const
   p.kpe_out = static_cast<__nv_bfloat16*>(kpe_out);
   p.n = n;
   p.num_slots = num_pages * page_size;
-  return launched(mla::launch_gather(p, fp8, static_cast<cudaStream_t>(stream)));
+  return launched(mla::launch_gather(p, fp8, stream_of(stream)));
 }
 
 int copy_pages(void* a, void* b, int bytes_a, int bytes_b, const int32_t* src, const int32_t* dst,
@@ -104,7 +109,7 @@ int copy_pages(void* a, void* b, int bytes_a, int bytes_b, const int32_t* src, c
   p.page_size = page_size;
   p.bytes_a = bytes_a;
   p.bytes_b = bytes_b;
-  return launched(mla::launch_copy_pages(p, static_cast<cudaStream_t>(stream)));
+  return launched(mla::launch_copy_pages(p, stream_of(stream)));
 }
 
 int check_pool(const mla_pool* pool) {
@@ -226,7 +231,7 @@ int mla_pages_extend(const mla_pool* pool, const int32_t* rows, const int32_t* n
   p.slots = slots;
   p.capacity = capacity;
   p.results = results;
-  return launched(mla::launch_pages_extend(p, w, static_cast<cudaStream_t>(stream)));
+  return launched(mla::launch_pages_extend(p, w, stream_of(stream)));
 }
 
 int mla_pages_fork(const mla_pool* pool, const int32_t* parents, const int32_t* children, int n, int32_t* src,
@@ -247,7 +252,7 @@ int mla_pages_fork(const mla_pool* pool, const int32_t* parents, const int32_t* 
   p.dst = dst;
   p.copy_tokens = copy_tokens;
   p.results = results;
-  return launched(mla::launch_pages_fork(p, w, static_cast<cudaStream_t>(stream)));
+  return launched(mla::launch_pages_fork(p, w, stream_of(stream)));
 }
 
 int mla_pages_free(const mla_pool* pool, const int32_t* rows, int n, void* stream) {
@@ -259,7 +264,7 @@ int mla_pages_free(const mla_pool* pool, const int32_t* rows, int n, void* strea
   if (!rows) return MLA_ERR_NULL;
   mla::PoolParams p = params_of(pool, n);
   p.rows = rows;
-  return launched(mla::launch_pages_free(p, static_cast<cudaStream_t>(stream)));
+  return launched(mla::launch_pages_free(p, stream_of(stream)));
 }
 
 int mla_pages_compact(const mla_pool* pool, int32_t* counts, int32_t* src, int32_t* dst, void* workspace,
@@ -274,7 +279,7 @@ int mla_pages_compact(const mla_pool* pool, int32_t* counts, int32_t* src, int32
   p.counts = counts;
   p.src = src;
   p.dst = dst;
-  return launched(mla::launch_pages_compact(p, w, static_cast<cudaStream_t>(stream)));
+  return launched(mla::launch_pages_compact(p, w, stream_of(stream)));
 }
 
 }  // extern "C"

@@ -467,3 +467,32 @@ def test_what_a_call_allocates_belongs_to_its_stream(lib):
     assert torch.equal(taken.cpu(), torch.arange(8000, dtype=torch.int32))
     assert torch.equal(rotated, c["qp"])
     assert moves[0].tolist() == [8000, 0]
+
+
+def test_two_graphs_share_a_workspace(lib):
+    """Calls of other sizes captured into two graphs over one workspace, replayed in turn: nothing
+    in it carries over.  A third call allocates its workspace inside the capture."""
+    require_gpu()
+    xs = [make([60, 9, 0], [500, 130, 64], 16, 64, seed=50), make([3, 1, 40, 7], [900, 1, 40, 333], 24, 16, seed=51)]
+    cs = [{k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()} for x in xs]
+    ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+
+    def call(c, workspace):
+        return lib.mla_paged_prefill_fp8(c["qn"], c["qp"], c["kv"], c["qo"], c["kp"], c["ki"], c["scale"],
+                                         workspace=workspace)
+
+    want = [call(c, ws) for c in cs]
+    for w, x in zip(want, xs):
+        close(w, plain(x))
+    captured = []
+    for c, workspace in ((cs[0], ws), (cs[1], ws), (cs[0], None)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call(c, workspace)
+        captured.append((graph, got))
+    for i in (0, 1, 2, 1, 0, 0, 2):
+        graph, got = captured[i]
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i % 2]))

@@ -193,6 +193,15 @@ def _check_cuda(name, t, dtype):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _new(make, shape, dtype, like, stream):
+    """A new tensor on the device of ``like``.  It belongs to the stream that the call runs on:
+    memory of another one could still be in use there, or be zeroed too late."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
+
+
 def _cache_geometry(ckv_cache, kpe_cache):
     if ckv_cache.dim() != 3 or ckv_cache.shape[-1] != HEAD_DIM_CKV:
         raise ValueError("ckv_cache must be [num_pages, page_size, 512]")
@@ -221,9 +230,9 @@ def _call(prefill, q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, kv_indptr, kv_
                      total_q=rows if prefill else 0, num_workers=num_workers)
     dev = q_nope.device
     if out is None:
-        out = torch.empty(rows, heads, HEAD_DIM_CKV, dtype=torch.bfloat16, device=dev)
+        out = _new(torch.empty, (rows, heads, HEAD_DIM_CKV), torch.bfloat16, q_nope, stream)
     if lse is None:
-        lse = torch.empty(rows, heads, dtype=torch.float32, device=dev)
+        lse = _new(torch.empty, (rows, heads), torch.float32, q_nope, stream)
     _check_cuda("out", out, torch.bfloat16)
     _check_cuda("lse", lse, torch.float32)
     if out.shape != (rows, heads, HEAD_DIM_CKV) or lse.shape != (rows, heads):
@@ -232,7 +241,7 @@ def _call(prefill, q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, kv_indptr, kv_
     if need == 0:
         raise MlaError(-2, "mla_workspace_bytes")
     if workspace is None:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+        workspace = _new(torch.zeros, need, torch.uint8, q_nope, stream)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     sp = ctypes.c_void_p(stream.cuda_stream)
@@ -289,9 +298,9 @@ def mla_paged_decode_mtp(q_nope, q_pe, ckv_cache, kpe_cache, kv_indptr, kv_indic
     dims = make_dims(batch, heads, num_pages, page_size, kv_indices.numel(), num_workers=num_workers)
     dev = q_nope.device
     if out is None:
-        out = torch.empty(batch, q_len, heads, HEAD_DIM_CKV, dtype=torch.bfloat16, device=dev)
+        out = _new(torch.empty, (batch, q_len, heads, HEAD_DIM_CKV), torch.bfloat16, q_nope, stream)
     if lse is None:
-        lse = torch.empty(batch, q_len, heads, dtype=torch.float32, device=dev)
+        lse = _new(torch.empty, (batch, q_len, heads), torch.float32, q_nope, stream)
     _check_cuda("out", out, torch.bfloat16)
     _check_cuda("lse", lse, torch.float32)
     if out.shape != (batch, q_len, heads, HEAD_DIM_CKV) or lse.shape != (batch, q_len, heads):
@@ -300,7 +309,7 @@ def mla_paged_decode_mtp(q_nope, q_pe, ckv_cache, kpe_cache, kv_indptr, kv_indic
     if need == 0:
         raise MlaError(-2, "mla_workspace_bytes_mtp")
     if workspace is None:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+        workspace = _new(torch.zeros, need, torch.uint8, q_nope, stream)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
@@ -332,9 +341,9 @@ def mla_paged_decode_sparse(q_nope, q_pe, ckv_cache, kpe_cache, indices, sm_scal
     dims = make_dims(rows, heads, num_pages, page_size, rows * topk, num_workers=num_workers)
     dev = q_nope.device
     if out is None:
-        out = torch.empty(rows, heads, HEAD_DIM_CKV, dtype=torch.bfloat16, device=dev)
+        out = _new(torch.empty, (rows, heads, HEAD_DIM_CKV), torch.bfloat16, q_nope, stream)
     if lse is None:
-        lse = torch.empty(rows, heads, dtype=torch.float32, device=dev)
+        lse = _new(torch.empty, (rows, heads), torch.float32, q_nope, stream)
     _check_cuda("out", out, torch.bfloat16)
     _check_cuda("lse", lse, torch.float32)
     if out.shape != (rows, heads, HEAD_DIM_CKV) or lse.shape != (rows, heads):
@@ -343,7 +352,7 @@ def mla_paged_decode_sparse(q_nope, q_pe, ckv_cache, kpe_cache, indices, sm_scal
     if need == 0:
         raise MlaError(-2, "mla_workspace_bytes")
     if workspace is None:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+        workspace = _new(torch.zeros, need, torch.uint8, q_nope, stream)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
@@ -383,9 +392,9 @@ def _fp8_call(name, q_nope, q_pe, kv_fp8, kv_indptr, kv_indices, topk, sm_scale,
     dims = make_dims(rows, heads, num_pages, page_size, n_idx, num_workers=num_workers)
     dev = q_nope.device
     if out is None:
-        out = torch.empty(rows, heads, HEAD_DIM_CKV, dtype=torch.bfloat16, device=dev)
+        out = _new(torch.empty, (rows, heads, HEAD_DIM_CKV), torch.bfloat16, q_nope, stream)
     if lse is None:
-        lse = torch.empty(rows, heads, dtype=torch.float32, device=dev)
+        lse = _new(torch.empty, (rows, heads), torch.float32, q_nope, stream)
     _check_cuda("out", out, torch.bfloat16)
     _check_cuda("lse", lse, torch.float32)
     if out.shape != (rows, heads, HEAD_DIM_CKV) or lse.shape != (rows, heads):
@@ -394,7 +403,7 @@ def _fp8_call(name, q_nope, q_pe, kv_fp8, kv_indptr, kv_indices, topk, sm_scale,
     if need == 0:
         raise MlaError(-2, "mla_workspace_bytes")
     if workspace is None:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+        workspace = _new(torch.zeros, need, torch.uint8, q_nope, stream)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     sp = ctypes.c_void_p(stream.cuda_stream)
@@ -441,8 +450,8 @@ def block_table_to_csr(block_table, seq_lens, page_size, capacity=None, stream=N
     if capacity is None:
         capacity = batch * max_blocks * page_size
     dev = block_table.device
-    kv_indptr = torch.empty(batch + 1, dtype=torch.int32, device=dev)
-    kv_indices = torch.empty(max(int(capacity), 1), dtype=torch.int32, device=dev)
+    kv_indptr = _new(torch.empty, batch + 1, torch.int32, block_table, stream)
+    kv_indices = _new(torch.empty, max(int(capacity), 1), torch.int32, block_table, stream)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
@@ -474,9 +483,9 @@ def mla_paged_decode_block_table(q_nope, q_pe, ckv_cache, kpe_cache, block_table
     dims = make_dims(batch, heads, num_pages, page_size, 0, num_workers=num_workers)
     dev = q_nope.device
     if out is None:
-        out = torch.empty(batch, heads, HEAD_DIM_CKV, dtype=torch.bfloat16, device=dev)
+        out = _new(torch.empty, (batch, heads, HEAD_DIM_CKV), torch.bfloat16, q_nope, stream)
     if lse is None:
-        lse = torch.empty(batch, heads, dtype=torch.float32, device=dev)
+        lse = _new(torch.empty, (batch, heads), torch.float32, q_nope, stream)
     _check_cuda("out", out, torch.bfloat16)
     _check_cuda("lse", lse, torch.float32)
     if out.shape != (batch, heads, HEAD_DIM_CKV) or lse.shape != (batch, heads):
@@ -485,7 +494,7 @@ def mla_paged_decode_block_table(q_nope, q_pe, ckv_cache, kpe_cache, block_table
     if need == 0:
         raise MlaError(-2, "mla_workspace_bytes_block_table")
     if workspace is None:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+        workspace = _new(torch.zeros, need, torch.uint8, q_nope, stream)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):

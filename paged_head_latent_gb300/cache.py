@@ -14,7 +14,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import (FP8_TOKEN_BYTES, HEAD_DIM_CKV, HEAD_DIM_KPE, MlaDims, MlaError, MlaPool, MlaRopeDims, _cache_geometry,
-               lib, make_dims)
+               _new, lib, make_dims)
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -75,15 +75,6 @@ def _ints(name, t, shape, index):
     _check(name, t, _I32, index)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} int32, got {list(t.shape)}")
-
-
-def _new(make, shape, dtype, like, stream):
-    """A new tensor on the device of ``like``.  It belongs to the stream that the call runs on:
-    memory of another one could still be in use there, or be zeroed too late."""
-    if stream is None:
-        return make(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=like.device)
 
 
 def _buffer(name, t, shape, dtype, like, stream):

@@ -373,7 +373,9 @@ int mla_cache_copy_pages_fp8(void* kv_fp8, const int32_t* src, const int32_t* ds
  *     MLA_ERR_NO_PAGES (nothing changes) if the entry needs pages and the free pages do not
  *     cover it together with all earlier valid entries
  *   new_indptr [n + 1]: offsets of the granted tokens (refused entries add none), packed in
- *     list order (the qo_indptr of a prefill)
+ *     list order (the qo_indptr of a prefill).  Behind a refused entry the offsets are not
+ *     those of the requested counts: inputs that were packed by the requested counts have to
+ *     be repacked by new_indptr before they are written to the slots or attended
  *   slots [capacity]: their token slots (the slots of mla_rope_append); positions past
  *     the last granted token get -1, tokens past the capacity are counted but not written
  * mla_pages_fork: row children[i] (empty) becomes a copy of row parents[i]: full pages are

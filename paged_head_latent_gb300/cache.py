@@ -334,7 +334,8 @@ def mla_pages_extend(block_table, seq_lens, ref_count, rows, new_tokens, page_si
     """Row rows[i] grows by new_tokens[i] tokens.  Returns (new_indptr [n + 1], slots
     [capacity], results [n]): where the granted tokens of every entry are in ``slots``, their
     token slots (-1 past the last), and 0 or the status of a refused entry (-6 bad index,
-    -11 too few free pages)."""
+    -11 too few free pages).  A refused entry has no slots and the later ones move up: inputs
+    packed by ``new_tokens`` have to be repacked by new_indptr before they go with ``slots``."""
     pool, index = _pool(block_table, seq_lens, ref_count, page_size)
     n = _entries("rows", rows, index)
     _ints("new_tokens", new_tokens, (n,), index)

@@ -394,7 +394,9 @@ int mla_cache_copy_pages_fp8(void* kv_fp8, const int32_t* src, const int32_t* ds
  *
  * n entries, all arrays int32 on the device, outputs as described.  workspace >=
  * mla_workspace_bytes_pages(pool, n) bytes (compact: n = 0), 16-byte aligned; nothing in
- * it carries over between calls.  Calls on the same pool or workspace must be ordered.
+ * it carries over between calls, and its first 256 bytes are left as they are, so it may be
+ * the workspace of an attention call, whose status word stays what it was.  Calls on the
+ * same pool or workspace must be ordered.
  * MLA_ERR_DIMS: negative sizes, page_size < 1, max_blocks * page_size or num_pages *
  * page_size over INT32_MAX.
  */

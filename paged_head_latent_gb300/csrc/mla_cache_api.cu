@@ -139,13 +139,15 @@ mla::PoolParams params_of(const mla_pool* pool, int n) {
   return p;
 }
 
-// Workspace: free-page bitmap, free pages before each of its words and spans, claims, pages taken,
-// then the entries' decisions.
+// Workspace: 256 bytes left alone (the attention calls' status word, where the workspace serves them
+// too), free-page bitmap, free pages before each of its words and spans, claims, pages taken, then
+// the entries' decisions.
 struct PoolLayout {
-  size_t before, base, claim, pages, old_len, first, total;
+  size_t bits, before, base, claim, pages, old_len, first, total;
   PoolLayout(const mla_pool* pool, int n) {
     const size_t words = ((size_t)pool->num_pages + 31) / 32;
-    before = mla::align_up(words * 4, 256);
+    bits = 256;
+    before = bits + mla::align_up(words * 4, 256);
     base = before + mla::align_up(words * 4, 256);
     claim = base + mla::align_up(words / 256 * 4 + 4, 256);
     pages = claim + mla::align_up((size_t)pool->max_rows * 4, 256);
@@ -160,7 +162,7 @@ int work_of(const mla_pool* pool, int n, void* workspace, size_t bytes, mla::Poo
   if (!workspace || bytes < lay.total) return MLA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return MLA_ERR_ALIGN;
   auto* ws = static_cast<uint8_t*>(workspace);
-  w->bits = reinterpret_cast<uint32_t*>(ws);
+  w->bits = reinterpret_cast<uint32_t*>(ws + lay.bits);
   w->before = reinterpret_cast<int32_t*>(ws + lay.before);
   w->base = reinterpret_cast<int32_t*>(ws + lay.base);
   w->claim = reinterpret_cast<int32_t*>(ws + lay.claim);

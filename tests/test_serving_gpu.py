@@ -125,3 +125,24 @@ def test_the_readmes_step(lib, rows, new, captured):
     for r in range(ROWS):
         at = [pool.table[r][k // PS] * PS + k % PS for k in range(pool.lens[r])]
         assert torch.equal(cache[at], tokens.get(r, old[:0]))
+
+
+@pytest.mark.parametrize("pages", [600, 40000])
+def test_one_workspace_for_the_pool_and_the_attention(lib, pages):
+    """The pool's calls leave the attention's status word alone: no error is read that no attention
+    call made, and one that was made is still there."""
+    require_gpu()
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    arrays = (_i([[-1] * 9] * 5), _i([0] * 5), _i([0] * pages))
+    bad = torch.ones(1, 1, 512, dtype=torch.bfloat16).cuda()
+    attend = (bad, bad[..., :64].contiguous(), torch.zeros(1, 4, 656, dtype=torch.uint8).cuda(), _i([0, 1]), _i([0, 2]),
+              _i([0, -1]), 1.0)
+    for flags, status in ((0, 0), (lib.MLA_VALIDATE, -6)):
+        lib.mla_paged_prefill_fp8(*attend, workspace=ws, flags=flags)
+        _, _, results = lib.mla_pages_extend(*arrays, _i([0, 3]), _i([9, 6]), PS, 15, workspace=ws)
+        assert results.tolist() == [0, 0]
+        lib.mla_pages_fork(*arrays, _i([0]), _i([4]), PS, workspace=ws)
+        lib.mla_pages_free(*arrays, _i([0, 4]), PS)
+        lib.mla_pages_compact(*arrays, PS, workspace=ws)
+        assert lib.read_device_status(ws) == status
+        lib.mla_pages_free(*arrays, _i([3]), PS)

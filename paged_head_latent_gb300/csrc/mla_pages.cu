@@ -269,10 +269,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PoolParams p, PoolWo
       p.results[i] = granted ? MLA_OK : ok ? MLA_ERR_NO_PAGES : MLA_ERR_BAD_INDEX;
       w.old_len[i] = granted ? e.len : -1;
       w.first[i] = (int32_t)first;
-      if (!kFork) p.new_indptr[i] = (int32_t)at;
+      if (!kFork) p.new_indptr[i] = (int32_t)min(at, 0x7fffffffLL);
     }
   }
-  if (!kFork && threadIdx.x == 0) p.new_indptr[p.n] = (int32_t)new_run;
+  // Rows that share a partly filled page that is counted once (no call of the pool makes such) could
+  // be granted more tokens than an int holds; no slot is written past the capacity, so none there.
+  if (!kFork && threadIdx.x == 0) p.new_indptr[p.n] = (int32_t)min(new_run, 0x7fffffffLL);
   __syncthreads();
   free.list(taken);
 }
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kApplyThreads) extend_kernel(PoolParams p, Poo
     }
     const int last = have > 0 && len % p.page_size != 0 ? table[have - 1] : 0;
     const long long at = p.new_indptr[i];
-    for (int k = threadIdx.x; at >= 0 && k < add && at + k < p.capacity; k += kApplyThreads) {
+    for (int k = threadIdx.x; k < add && at + k < p.capacity; k += kApplyThreads) {
       const int pos = len + k, block = pos / p.page_size;
       const int page = block < have ? last : pages[block - have];
       p.slots[at + k] = page * p.page_size + pos % p.page_size;

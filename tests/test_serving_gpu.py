@@ -146,3 +146,18 @@ def test_one_workspace_for_the_pool_and_the_attention(lib, pages):
         lib.mla_pages_compact(*arrays, PS, workspace=ws)
         assert lib.read_device_status(ws) == status
         lib.mla_pages_free(*arrays, _i([3]), PS)
+
+
+def test_more_tokens_than_an_int_holds(lib):
+    """Rows that all hold one page that is counted once, which no call of the pool makes: the
+    offsets stay at the largest int, and no slot is written outside the buffer."""
+    require_gpu()
+    rows, ps = 3000, 1 << 20
+    table, lens, refs = _i([[0]] * rows), _i([1] * rows), _i([1] + [0] * 1999)
+    guard = torch.full((300,), 7, dtype=torch.int32, device="cuda")
+    ptr, slots, results = lib.mla_pages_extend(table, lens, refs, torch.arange(rows, dtype=torch.int32, device="cuda"),
+                                               _i([ps - 1] * rows), ps, 100, slots=guard[100:200])
+    assert not results.any() and (lens == ps).all()
+    assert ptr.tolist() == [min(i * (ps - 1), 2 ** 31 - 1) for i in range(rows + 1)]
+    assert slots.tolist() == list(range(1, 101))
+    assert (guard[:100] == 7).all() and (guard[200:] == 7).all()

@@ -300,6 +300,7 @@ int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_f
  *         written (its query is rotated all the same).  Slots named by several tokens end
  *         up with a mixture of those tokens' values: name a slot once.
  *   q_out [tokens, H, 64] bf16, contiguous; may be q_pe itself if q_pe is contiguous
+ *         (MLA_ERR_DIMS otherwise), and must not overlap it in any other way
  * Strides are in elements and multiples of 8; all tensor pointers 16-byte aligned
  * (MLA_ERR_ALIGN).  MLA_ERR_DIMS if the sections do not add up to 32 pairs over num_axes
  * axes.  One launch.

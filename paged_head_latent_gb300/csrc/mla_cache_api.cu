@@ -46,6 +46,11 @@ int rope_append(const void* q_pe, const void* ckv, const void* k_pe, const int32
   if (d->num_qo_heads > 0 && (!aligned16(q_pe) || !aligned16(q_out))) return MLA_ERR_ALIGN;
   if (d->ckv_stride % 8 || d->kpe_stride % 8) return MLA_ERR_ALIGN;
   if (d->num_qo_heads > 0 && (d->q_stride_token % 8 || d->q_stride_head % 8)) return MLA_ERR_ALIGN;
+  // In place, a warp writes where it read only if the queries lie as the output does.
+  if (d->num_qo_heads > 0 && q_out == q_pe &&
+      ((d->num_qo_heads > 1 && d->q_stride_head != mla::kDimKpe) ||
+       (d->tokens > 1 && d->q_stride_token != (int64_t)d->num_qo_heads * mla::kDimKpe)))
+    return MLA_ERR_DIMS;
   mla::RopeParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q_pe);
   p.ckv = static_cast<const __nv_bfloat16*>(ckv);

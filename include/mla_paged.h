@@ -270,7 +270,8 @@ int mla_noalloc_read_status(void* stream);
  * it and changes no other row.
  *   workspace >= mla_workspace_bytes_prefill_staged(dims) bytes, zero-filled before its first
  *   use; it holds the staged keys (1152 bytes for each of dims->num_kv_indices, plus up to
- *   128 keys per request) and one 256 KB fragment pair per worker.
+ *   128 keys per request) and one 256 KB fragment pair per worker.  Calls whose staged keys
+ *   number 2^31 or more are refused (MLA_ERR_DIMS; their workspace size reads 0).
  * mla_paged_prefill_fp8 is the same over the FP8 cache of mla_paged_decode_fp8 (every latent
  * value read as the same BF16 number), with the same workspace size.
  */

@@ -84,6 +84,7 @@ struct ChunkLayout {
     kpe = ckv + (size_t)tiles * kChunkKeys * kDimCkv * 2;
     total = align_up(kpe + (size_t)tiles * kChunkKeys * kDimKpe * 2, 256);
   }
+  bool addressable() const { return tiles * kChunkKeys < (1LL << 31); }  // a staged row is a tensor-map coordinate
 };
 
 // The three launches of a call: stage the keys and plan, attend, merge split blocks.

@@ -427,8 +427,7 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
   int G = 0;
   if ((st = resolve_workers(dims, &G)) != MLA_OK) return st;
   const mla::ChunkLayout lay(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices);
-  // (a staged row is a tensor-map coordinate)
-  if (lay.tiles * mla::kChunkKeys >= (1LL << 31)) return MLA_ERR_DIMS;
+  if (!lay.addressable()) return MLA_ERR_DIMS;
   if (!workspace || workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return MLA_ERR_ALIGN;
   DeviceInfo info;
@@ -511,7 +510,8 @@ size_t mla_workspace_bytes_prefill_staged(const mla_dims* dims) {
   if (check_dims(dims, true) != MLA_OK) return 0;
   int G = 0;
   if (resolve_workers(dims, &G) != MLA_OK) return 0;
-  return mla::ChunkLayout(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices).total;
+  const mla::ChunkLayout lay(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices);
+  return lay.addressable() ? lay.total : 0;
 }
 
 int mla_paged_prefill_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,

@@ -267,10 +267,11 @@ int mla_noalloc_read_status(void* stream);
  * kv_indptr[batch]: the rows behind the last request are left as they were.  (MLA_VALIDATE
  * reports both, as for mla_paged_prefill.)  A listed slot outside the cache is not a key.
  * A key that holds a value that is not finite makes out and lse NaN in the rows that see
- * it and changes no other row.
+ * it and changes no other row.  (mla_paged_prefill lets such a value run through its
+ * arithmetic: in the rows that see it some columns of out, and lse, may stay finite.)
  *   workspace >= mla_workspace_bytes_prefill_staged(dims) bytes, zero-filled before its first
  *   use; it holds the staged keys (1152 bytes for each of dims->num_kv_indices, plus up to
- *   128 keys per request) and one 256 KB fragment pair per worker.  Calls whose staged keys
+ *   128 keys per request) and two fragments of 256 KB (513 KB with their lse) per worker.  Calls whose staged keys
  *   number 2^31 or more are refused (MLA_ERR_DIMS; their workspace size reads 0).
  * mla_paged_prefill_fp8 is the same over the FP8 cache of mla_paged_decode_fp8 (every latent
  * value read as the same BF16 number), with the same workspace size.

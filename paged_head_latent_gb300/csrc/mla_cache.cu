@@ -93,8 +93,10 @@ __device__ __forceinline__ uint4 quantise16(const uint4 (&raw)[2], float* scale)
 //                l the pairs 4(l % 8) .. + 3 of head l / 8;
 //   half-split:  pair i = elements i, i + 32; 8 heads per instruction pair, lane l the pairs
 //                8(l % 4) .. + 7 of head l / 4.
-// Bound by HBM: 8192 tokens of 128 heads (287 MB) take 47.4 us, 6.06 TB/s, 0.90 of the measured
-// copy rate; 64 tokens take about 4 us, a launch and two round trips to memory.
+// Bound by HBM: 8192 tokens of 128 heads (287 MB) take 47.1 us, 6.1 TB/s, 0.91 of the measured
+// copy rate; 8000 into an FP8 cache 45.3 us, where the bytes take 41.3; 8000 of one head, whose cache
+// rows are most of it, 6.4 us (bf16, bytes 3.1) and 10 (FP8, bytes 2.5).  64 tokens take 2.5 us, 2.9
+// into an FP8 cache (calls back to back in a graph): a launch and two round trips to memory.
 template <bool kInterleaved, bool kFp8>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p) {
   // One warp does the block's double-precision work: with every warp doing it, 8000 tokens of
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
 // Tokens read by slot into contiguous bf16 rows, kTok tokens of a warp in flight.  Tokens whose
 // slot is outside the cache become zero rows.  Bound by HBM: 263K FP8 tokens on 64-slot pages
 // (477 MB) take 74.5 us, 6.4 TB/s, 0.96 of the measured copy rate (two tokens in flight 97 us,
-// eight 78; with a grid of resident blocks 84).
+// eight 78; with a grid of resident blocks 84), 263K bf16 tokens (607 MB) 88 us, the copy rate.
 template <bool kFp8, int kTok>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) {
   const int lane = threadIdx.x & 31;

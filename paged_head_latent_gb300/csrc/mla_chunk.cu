@@ -25,9 +25,10 @@
 // sustained 62 bytes a cycle and SM for these boxes, which is 2250 cycles a tile.
 //
 // What bounds it.  A tile takes 2470 cycles with its share of the blocks' starts and ends (four
-// prompts, 128 heads, 22 tiles a block: 870 us, 1.72 PFLOP/s, 0.90 of the measured bf16 burst rate, at
-// the 1.6 GHz that the power limit leaves; one prompt of 256 tokens over 4096 keys: tensor pipe
-// 80 % active).  Shared memory is the next limit: operands, loads and P move 392 KB a tile.
+// prompts, 128 heads, 22 tiles a block: 850 to 870 us with staging and merge, 1.72 to 1.76 PFLOP/s,
+// 0.90 to 0.92 of the measured bf16 burst rate, at the 1.6 GHz that the power limit leaves; one prompt of 256 tokens over 4096 keys: tensor pipe
+// 80 % active).  What writes shared memory, the loads and P, is 152 KB a tile, 1216 cycles at 128
+// bytes a cycle; the products read their operands besides, at a rate that was not measured.
 //
 // The tensor pipe's order is S(j+1), then O += P(j) V(j): the softmax of tile j runs while S(j+1)
 // is computed.
@@ -410,7 +411,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 16; ++k) {
         const float a = fast_exp2(fmaf(s[2 * k], mul, -m)), b = fast_exp2(fmaf(s[2 * k + 1], mul, -m));
         sum[k & 3] += a + b;
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);  // the tensor cores' operand type
+        // The operand type beside a bf16 V: a weight is off by 2^-8 of itself at most, its sum keeps
+        // all bits.  On the measured chunks the output is within 2.0e-3 of 64 bits, 1.7e-3 with float32
+        // weights; weights in two bf16 parts would double the product.
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         pk[k] = *reinterpret_cast<const uint32_t*>(&h);
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);

@@ -310,6 +310,11 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
 }  // namespace
 
 cudaError_t launch_chunk_stage(const ChunkParams& p, bool fp8, cudaStream_t stream) {
+  // Blocks walk the parts in use, so a buffer longer than its list costs little.  With a block for
+  // every part of the buffer and no loop the whole call takes 170 us instead of 172 for 301K keys and
+  // 980 instead of 988 for 2.1 million, but 47 instead of 34 for 32K keys in a buffer of 524K, and
+  // 93 instead of 34 in one of 2 million (one token a request, 16 heads); caps of 64 and 128
+  // blocks an SM gain nothing on the full lists and take 40 and 47 on the third.
   const int parts = p.tiles * (kChunkKeys / kStageKeys);  // (tiles * 128 is below 2^31)
   const int grid = 1 + (parts < 152 * 32 ? parts : 152 * 32);
   if (fp8) chunk_stage_kernel<true><<<grid, kStageThreads, 0, stream>>>(p);

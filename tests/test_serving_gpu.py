@@ -1,6 +1,7 @@
 """The serving step as the README prints it: the very lines are run, eagerly and captured, with
 entries that the pool refuses in the middle of the step."""
 
+import copy
 import os
 
 import numpy as np
@@ -46,7 +47,7 @@ def test_the_readmes_step(lib, rows, new, captured):
     require_gpu()
     once, step = readme_lines()
     g = torch.Generator().manual_seed(len(rows) + new[0])
-    n, total, max_keys = len(rows), 24, ROWS * BLOCKS * PS
+    n, total = len(rows), 24
     lens0 = [9, 20, 4, 1, 0, 7, 0, 12]  # (row 1 fills its table)
     start = np.concatenate([[0], np.cumsum(new)])
     inputs = dict(q_nope=_bf(g, total, HEADS, 512), q_pe=_bf(g, total, HEADS, 64), ckv=_bf(g, total, 512),
@@ -54,7 +55,7 @@ def test_the_readmes_step(lib, rows, new, captured):
     for i, (r, c) in enumerate(zip(rows, new)):
         first = lens0[r] if 0 <= r < ROWS else 0
         inputs["positions"][start[i]:start[i + 1]] = first + torch.arange(c, dtype=torch.int32)
-    ns = dict(torch=torch, mla=lib, n=n, total=total, max_keys=max_keys, heads=HEADS, num_pages=PAGES, page_size=PS,
+    ns = dict(torch=torch, mla=lib, n=n, total=total, heads=HEADS, num_pages=PAGES, page_size=PS,
               table=_i([[-1] * BLOCKS] * ROWS), lens=_i([0] * ROWS), refs=_i([0] * PAGES), rows=_i(rows),
               new_tokens=_i(new), parents=_i([5, 0, 2, 1]), children=_i([4, 6, 6, 2]), ended=_i([0, 7, -1]),
               inv_freq=FREQ.cuda(), sm_scale=192 ** -0.5,
@@ -73,6 +74,10 @@ def test_the_readmes_step(lib, rows, new, captured):
     for r in order:
         tokens[r] = old[at:at + lens0[r]]
         at += lens0[r]
+    # Room for the keys of the granted entries and no more.
+    dry = copy.deepcopy(pool)
+    granted = [r for r, st in zip(rows, dry.extend(rows, new, total)[2]) if st == 0]
+    ns["max_keys"] = sum(dry.lens[r] for r in granted)
     exec(once, ns)
     state = [t.clone() for t in (*arrays, ns["kv_fp8"])]
     given = dict(ns)

@@ -288,6 +288,112 @@ int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_f
                           void* stream);
 
 /*
+ * Attention with a sliding window and sinks: query i of a request with q_len new tokens and
+ * kv_len keys stands at position p = kv_len - q_len + i and sees its keys t <= p of which
+ *   t > p - window (the last `window` ones, its own among them) or t < sinks (the first ones),
+ * with window >= 1 and sinks >= 0 (else MLA_ERR_DIMS).  mla_paged_decode_window has one query per
+ * request (arguments of mla_paged_decode, rows = dims->batch); mla_paged_prefill_window ragged
+ * chunks of them (arguments of mla_paged_prefill_staged).  The lists name all keys of a
+ * request, seen or not: positions count from their start.  Keys that no query of the call sees
+ * are not read, so their values, and the slots listed for them, do not matter.  Rows that see
+ * no key get out = 0, lse = -inf; rows behind the last request are left as they were; a listed
+ * slot outside the cache is not a key; a key with a value that is not finite makes out and lse
+ * NaN in the rows that see it and changes no other row.
+ *   workspace >= mla_workspace_bytes_window(dims, window, sinks, is_prefill) bytes (is_prefill:
+ *   1 for the prefill calls), zero-filled before its first use.  It holds a copy of the keys
+ *   seen: 1152 bytes a key, in whole tiles of 128 for at most min(num_kv_indices + 127 per
+ *   request, total_q + (window + sinks + 510) per request) keys.  Calls whose staged keys would number 2^31 or more are
+ *   refused (MLA_ERR_DIMS; their workspace size reads 0).
+ * The _fp8 calls read the FP8 cache of mla_paged_decode_fp8.
+ */
+size_t mla_workspace_bytes_window(const mla_dims* dims, int window, int sinks, int is_prefill);
+int mla_paged_decode_window(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                            const int32_t* kv_indptr, const int32_t* kv_indices, int window, int sinks, float sm_scale,
+                            void* out, float* lse, const mla_dims* dims, void* workspace, size_t workspace_bytes,
+                            int flags, void* stream);
+int mla_paged_decode_window_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* kv_indptr,
+                                const int32_t* kv_indices, int window, int sinks, float sm_scale, void* out, float* lse,
+                                const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream);
+int mla_paged_prefill_window(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                             const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices, int window,
+                             int sinks, float sm_scale, void* out, float* lse, const mla_dims* dims, void* workspace,
+                             size_t workspace_bytes, int flags, void* stream);
+int mla_paged_prefill_window_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
+                                 const int32_t* kv_indptr, const int32_t* kv_indices, int window, int sinks,
+                                 float sm_scale, void* out, float* lse, const mla_dims* dims, void* workspace,
+                                 size_t workspace_bytes, int flags, void* stream);
+
+/*
+ * Attention of requests that share a prefix, whose keys are listed, read and multiplied once for
+ * blocks of 128 (token, head) rows of the group.  Group g has the requests group_indptr[g] ..
+ * group_indptr[g + 1] - 1 and the prefix keys prefix_indices[prefix_indptr[g] ..
+ * prefix_indptr[g + 1]]; kv_indptr and kv_indices list the keys that each request has of its
+ * own, the new tokens' among them.  A query sees every key of its group's prefix and, of its own
+ * m keys, query i of q_len sees the first m - q_len + i + 1 (decode: all).  So the results are those of
+ * mla_paged_decode, or mla_paged_prefill_staged, on lists of the prefix followed by the own
+ * keys (but for rounding).
+ *   group_indptr, prefix_indptr [groups + 1] int32; groups may be empty, of one request, or have
+ *   an empty prefix.  A request in no group is left out: its rows stay as they were.
+ *   prefix_indices [num_prefix_indices] int32 token slots; like kv_indices it may be longer than
+ *   its list
+ *   mla_paged_decode_shared has one query per request (rows = dims->batch);
+ *   mla_paged_prefill_shared ragged chunks, qo_indptr as for mla_paged_prefill_staged.
+ *   workspace >= mla_workspace_bytes_shared(dims, groups, num_prefix_indices, is_prefill) bytes,
+ *   zero-filled before its first use: 1152 bytes for each prefix index and each of
+ *   dims->num_kv_indices, and up to 128 keys per group and request.  Staged keys of 2^31 or more are
+ *   refused (MLA_ERR_DIMS; their workspace size reads 0).
+ * Empty rows, rows behind the last request, slots outside the cache and keys that are not finite:
+ * as for mla_paged_prefill_window.  MLA_VALIDATE checks both lists and the groups.
+ * The _fp8 calls read the FP8 cache of mla_paged_decode_fp8.
+ */
+size_t mla_workspace_bytes_shared(const mla_dims* dims, int groups, int num_prefix_indices, int is_prefill);
+int mla_paged_decode_shared(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                            const int32_t* group_indptr, int groups, const int32_t* prefix_indptr,
+                            const int32_t* prefix_indices, int num_prefix_indices, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, float sm_scale, void* out, float* lse, const mla_dims* dims,
+                            void* workspace, size_t workspace_bytes, int flags, void* stream);
+int mla_paged_decode_shared_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* group_indptr,
+                                int groups, const int32_t* prefix_indptr, const int32_t* prefix_indices,
+                                int num_prefix_indices, const int32_t* kv_indptr, const int32_t* kv_indices,
+                                float sm_scale, void* out, float* lse, const mla_dims* dims, void* workspace,
+                                size_t workspace_bytes, int flags, void* stream);
+int mla_paged_prefill_shared(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                             const int32_t* qo_indptr, const int32_t* group_indptr, int groups,
+                             const int32_t* prefix_indptr, const int32_t* prefix_indices, int num_prefix_indices,
+                             const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out, float* lse,
+                             const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream);
+int mla_paged_prefill_shared_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
+                                 const int32_t* group_indptr, int groups, const int32_t* prefix_indptr,
+                                 const int32_t* prefix_indices, int num_prefix_indices, const int32_t* kv_indptr,
+                                 const int32_t* kv_indices, float sm_scale, void* out, float* lse, const mla_dims* dims,
+                                 void* workspace, size_t workspace_bytes, int flags, void* stream);
+
+/*
+ * The groups of a batch from its block table (the page pool's, whose forks share full pages), as
+ * the shared attention takes them.  With len_i = clamp(seq_lens[i], 0, max_blocks * page_size),
+ * row i is compared with row i - 1: the leading page ids that both have in common, among the
+ * pages that are full in both, hold s_i keys.  Row i joins row i - 1's group if s_i >=
+ * max(1, min_shared), else it opens the next one (rows that share pages should be neighbours).  A
+ * group shares the least s_i of the rows that joined it, a group of one row shares nothing.
+ *   group_indptr [batch + 1]: first row of every group; `batch` from the last group's end on, so
+ *     the attention may be called with groups = batch
+ *   prefix_indptr [batch + 1]: offsets of the groups' shared keys; the total from there on
+ *   prefix_indices [prefix_capacity]: their token slots, by the first row of the group
+ *   kv_indptr [batch + 1], kv_indices [capacity]: every row's keys behind the shared ones
+ * Slots as for mla_block_table_to_csr (-1 where they do not fit an int32).  Entries at or past a
+ * capacity, and behind the end of a list, are left as they were; the offsets still count
+ * entries past the capacity, and stay at 2^31 - 1 once they have reached it.  Three launches.
+ * For a step with several new tokens per row call it after the pool has been extended: pages
+ * with new tokens are never shared.
+ * MLA_ERR_DIMS: negative sizes, page_size < 1, max_blocks * page_size or a capacity above
+ * INT32_MAX.
+ */
+int mla_block_table_to_shared_csr(const int32_t* block_table, const int32_t* seq_lens, int batch, int max_blocks,
+                                  int page_size, int min_shared, int32_t* group_indptr, int32_t* prefix_indptr,
+                                  int32_t* prefix_indices, long long prefix_capacity, int32_t* kv_indptr,
+                                  int32_t* kv_indices, long long capacity, void* stream);
+
+/*
  * Rotary positions and the cache write, for the new tokens of a step.  With 32 pairs of
  * elements (interleaved: elements 2i and 2i + 1; else elements i and i + 32) and
  * angle = positions[axis(i)][t] * inv_freq[i], pair (a, b) of every query head of token t

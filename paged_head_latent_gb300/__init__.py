@@ -90,6 +90,36 @@ _SIGNATURES = [
     ("mla_paged_prefill_fp8", ctypes.c_int,
      [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P, ctypes.c_size_t, ctypes.c_int,
       _P]),
+    ("mla_workspace_bytes_window", ctypes.c_size_t,
+     [ctypes.POINTER(MlaDims), ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    ("mla_paged_decode_window", ctypes.c_int,
+     [_P] * 6 + [ctypes.c_int, ctypes.c_int, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P, ctypes.c_size_t,
+                 ctypes.c_int, _P]),
+    ("mla_paged_decode_window_fp8", ctypes.c_int,
+     [_P] * 5 + [ctypes.c_int, ctypes.c_int, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P, ctypes.c_size_t,
+                 ctypes.c_int, _P]),
+    ("mla_paged_prefill_window", ctypes.c_int,
+     [_P] * 7 + [ctypes.c_int, ctypes.c_int, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P, ctypes.c_size_t,
+                 ctypes.c_int, _P]),
+    ("mla_paged_prefill_window_fp8", ctypes.c_int,
+     [_P] * 6 + [ctypes.c_int, ctypes.c_int, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P, ctypes.c_size_t,
+                 ctypes.c_int, _P]),
+    ("mla_workspace_bytes_shared", ctypes.c_size_t,
+     [ctypes.POINTER(MlaDims), ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    ("mla_paged_decode_shared", ctypes.c_int,
+     [_P] * 5 + [ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P,
+                 ctypes.c_size_t, ctypes.c_int, _P]),
+    ("mla_paged_decode_shared_fp8", ctypes.c_int,
+     [_P] * 4 + [ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P,
+                 ctypes.c_size_t, ctypes.c_int, _P]),
+    ("mla_paged_prefill_shared", ctypes.c_int,
+     [_P] * 6 + [ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P,
+                 ctypes.c_size_t, ctypes.c_int, _P]),
+    ("mla_paged_prefill_shared_fp8", ctypes.c_int,
+     [_P] * 5 + [ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, ctypes.c_float, _P, _P, ctypes.POINTER(MlaDims), _P,
+                 ctypes.c_size_t, ctypes.c_int, _P]),
+    ("mla_block_table_to_shared_csr", ctypes.c_int,
+     [_P, _P] + [ctypes.c_int] * 4 + [_P, _P, _P, ctypes.c_longlong, _P, _P, ctypes.c_longlong, _P]),
     ("mla_rope_append", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(MlaRopeDims), _P]),
     ("mla_rope_append_fp8", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(MlaRopeDims), _P]),
     ("mla_cache_gather", ctypes.c_int, [_P, _P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P]),
@@ -651,3 +681,8 @@ from .cache import (mla_cache_copy_pages, mla_cache_copy_pages_fp8, mla_cache_ga
                     mla_cache_gather_fp8, mla_paged_prefill_fp8, mla_paged_prefill_staged, mla_pages_compact,
                     mla_pages_extend, mla_pages_fork, mla_pages_free, mla_rope_append, mla_rope_append_fp8,
                     workspace_bytes_pages, workspace_bytes_prefill_fp8, workspace_bytes_prefill_staged)
+# Attention over parts of the cache: windows with sinks, prefixes shared by several requests.
+from .parts import (block_table_to_shared_csr, mla_paged_decode_shared, mla_paged_decode_shared_fp8,  # noqa: E402
+                    mla_paged_decode_window, mla_paged_decode_window_fp8, mla_paged_prefill_shared,
+                    mla_paged_prefill_shared_fp8, mla_paged_prefill_window, mla_paged_prefill_window_fp8,
+                    workspace_bytes_shared, workspace_bytes_window)

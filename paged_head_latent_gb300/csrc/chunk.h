@@ -10,14 +10,25 @@ namespace mla {
 constexpr int kChunkKeys = 128;  // keys of a tile
 constexpr int kChunkRows = 128;  // query rows (token, head) of a block
 
-// 128 consecutive query rows of one request; row 0 of request b is (token 0, head 0).
+// Which keys a row sees.  kCausal: all of its request's keys up to its own token.  kWindow: of
+// those the last `window` and the first `sinks`.  kShared: all keys of its group's prefix list,
+// and of its request's own list those up to its own token.
+enum { kCausal = 0, kWindow = 1, kShared = 2 };
+
+// 128 consecutive query rows of one request (kShared: of one group); row 0 of request b is (token
+// 0, head 0).  Its tiles are two runs: kWindow, those with sinks and those from the first row's
+// window on; kShared, the prefix's, then those of its requests' own keys; else one run.
 struct ChunkBlock {
   int row0;      // first row of the block in [total_q * H]
-  int local0;    // ... and within its request
+  int local0;    // ... and within its request (kShared: unused)
   int rows;      // rows in use, 1..128
-  int tiles;     // key tiles that its last row sees (at least 1)
-  int tile0;     // first staged tile of the request
-  int seen;      // keys that token 0 of the request sees (may be <= 0)
+  int tiles;     // key tiles that its rows see (at least 1)
+  int tile0;     // staged tile of its first tile (causal: of the request's)
+  int seen;      // keys that token 0 of the request sees (may be <= 0; kShared: that a row sees of the first run)
+  int head;      // tiles of the first run (causal: unused, as what follows)
+  int rest0;     // kWindow: staged tile of the second run's first tile
+  int rest_key;  // kWindow: ... and its number among the request's key tiles
+  int req;       // kShared: the request of the first row
   long long cost0;  // cost units before this block
 };
 
@@ -58,25 +69,46 @@ struct ChunkParams {
   float* part_lse;      // [workers][2][128] base-2 lse of partial fragments
   float* part_o;        // [workers][2][512 / 4][128 rows][4]
   int tiles;            // staged tiles (an upper bound from the host's sizes)
+  // kWindow; kShared (qo_indptr may be null in both: a token per request)
+  int window, sinks;
+  int per_request;      // kWindow: tiles set aside for a request, or 0: for all of its keys
+  const int32_t* group_indptr;   // [groups + 1] requests
+  const int32_t* prefix_indptr;  // [groups + 1] prefix keys
+  const int32_t* prefix_indices;
+  int groups, num_prefix, prefix_tiles;  // prefix_tiles: staged tiles of the prefixes, before the own keys'
+  int32_t* own_tiles;   // [batch] own tiles of the requests before each
   int max_blocks;       // room in blocks
   unsigned long long wait_ns;
   int fault_skip_tile;
 };
+
+// ---- where staged tiles of the window and the shared attention lie (host and device)
+// kWindow.  A request's keys that any of its tokens sees are at most `sinks` and window + q_len - 1
+// more.  With those tiles set aside for every request, request b starts at staged tile
+// b * per + ceil(q0 / 128), which needs no prefix sum: a run of n keys touches at most
+// floor((n + 126) / 128) + 1 tiles, and ceil(q1 / 128) - ceil(q0 / 128) >= floor((q1 - q0) / 128).
+__host__ __device__ inline long long window_tiles_per_request(int window, int sinks) {
+  return ((long long)sinks + kChunkKeys - 1) / kChunkKeys + ((long long)window + kChunkKeys - 1) / kChunkKeys + 2;
+}
 
 struct ChunkMaps {
   CUtensorMap q_nope, q_pe, ckv, kpe;  // boxes of 64 rows x 64 columns, 128-byte swizzle
 };
 
 struct ChunkLayout {
-  size_t starts, merges, first_block, blocks, flags, part_lse, part_o, ckv, kpe, total;
+  size_t starts, merges, first_block, own_tiles, blocks, flags, part_lse, part_o, ckv, kpe, total;
   long long tiles, max_blocks;
   ChunkLayout(int workers, int heads, int batch, int total_q, int num_kv_indices) {
     tiles = ((long long)num_kv_indices + kChunkKeys - 1) / kChunkKeys + batch;
     max_blocks = ((long long)total_q * heads + kChunkRows - 1) / kChunkRows + batch;
+    place(workers, batch, 0);
+  }
+  void place(int workers, int lists, long long requests) {
     starts = 256;
     merges = align_up(starts + ((size_t)workers + 1) * sizeof(ChunkStart), 256);
     first_block = align_up(merges + (size_t)workers * sizeof(ChunkMerge), 256);
-    blocks = align_up(first_block + ((size_t)batch + 1) * sizeof(int32_t), 256);
+    own_tiles = align_up(first_block + ((size_t)lists + 1) * sizeof(int32_t), 256);
+    blocks = align_up(own_tiles + (size_t)requests * sizeof(int32_t), 256);
     flags = align_up(blocks + (size_t)max_blocks * sizeof(ChunkBlock), 256);
     part_lse = align_up(flags + (size_t)tiles * 32, 256);
     part_o = align_up(part_lse + (size_t)workers * 2 * kChunkRows * sizeof(float), 256);
@@ -84,12 +116,20 @@ struct ChunkLayout {
     kpe = ckv + (size_t)tiles * kChunkKeys * kDimCkv * 2;
     total = align_up(kpe + (size_t)tiles * kChunkKeys * kDimKpe * 2, 256);
   }
+  // The window and the shared attention: their own tiles, and room for blocks and own_tiles.
+  ChunkLayout(int workers, int heads, int lists, int total_q, long long staged_tiles, long long batch)
+      : tiles(staged_tiles) {
+    max_blocks = ((long long)total_q * heads + kChunkRows - 1) / kChunkRows + lists;
+    place(workers, lists, batch);
+  }
   bool addressable() const { return tiles * kChunkKeys < (1LL << 31); }  // a staged row is a tensor-map coordinate
 };
 
 // The three launches of a call: stage the keys and plan, attend, merge split blocks.
 cudaError_t launch_chunk_stage(const ChunkParams& p, bool fp8, cudaStream_t stream);
-cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_span_stage(const ChunkParams& p, int span, bool fp8, cudaStream_t stream);  // kWindow, kShared
+cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, int span, cudaStream_t stream);
+cudaError_t launch_validate_groups(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream);
 
 }  // namespace mla

@@ -15,6 +15,20 @@ cudaError_t launch_block_table_csr(const int32_t* block_table, const int32_t* se
                                    int page_size, int32_t* kv_indptr, int32_t* kv_indices, long long capacity,
                                    cudaStream_t stream);
 
+// Block table + sequence lengths -> groups that share leading pages, prefix lists and own lists.
+struct SharedTableParams {
+  const int32_t* block_table;  // [batch, max_blocks]
+  const int32_t* seq_lens;     // [batch]
+  int batch, max_blocks, page_size, min_shared;
+  int32_t* group_indptr;       // [batch + 1]
+  int32_t* prefix_indptr;      // [batch + 1]
+  int32_t* prefix_indices;     // [prefix_capacity]
+  int32_t* kv_indptr;          // [batch + 1]
+  int32_t* kv_indices;         // [capacity]
+  long long prefix_capacity, capacity;
+};
+cudaError_t launch_shared_tables(const SharedTableParams& p, cudaStream_t stream);
+
 // ---------------------------------------------------------------- the cache's writers and readers
 struct RopeParams {
   const __nv_bfloat16* q;    // [tokens, H, 64], strides in elements

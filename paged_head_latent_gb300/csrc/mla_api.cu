@@ -379,6 +379,23 @@ int mla_block_table_to_csr(const int32_t* block_table, const int32_t* seq_lens, 
   return MLA_OK;
 }
 
+int mla_block_table_to_shared_csr(const int32_t* block_table, const int32_t* seq_lens, int batch, int max_blocks,
+                                  int page_size, int min_shared, int32_t* group_indptr, int32_t* prefix_indptr,
+                                  int32_t* prefix_indices, long long prefix_capacity, int32_t* kv_indptr,
+                                  int32_t* kv_indices, long long capacity, void* stream) {
+  if (batch < 0 || max_blocks < 0 || page_size < 1 || min_shared < 0) return MLA_ERR_DIMS;
+  if (capacity < 0 || prefix_capacity < 0 || capacity > 0x7fffffffLL || prefix_capacity > 0x7fffffffLL)
+    return MLA_ERR_DIMS;
+  if ((long long)max_blocks * page_size > 0x7fffffffLL) return MLA_ERR_DIMS;
+  if (!group_indptr || !prefix_indptr || !kv_indptr) return MLA_ERR_NULL;
+  if (batch > 0 && (!seq_lens || (max_blocks > 0 && !block_table))) return MLA_ERR_NULL;
+  if ((capacity > 0 && !kv_indices) || (prefix_capacity > 0 && !prefix_indices)) return MLA_ERR_NULL;
+  cudaGetLastError();  // clear stale errors so the checks below see only ours
+  const mla::SharedTableParams p{block_table, seq_lens, batch, max_blocks, page_size, min_shared, group_indptr,
+                                 prefix_indptr, prefix_indices, kv_indptr, kv_indices, prefix_capacity, capacity};
+  return mla::launch_shared_tables(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_LAUNCH;
+}
+
 }  // extern "C"
 
 namespace {
@@ -409,24 +426,78 @@ bool block_table_dims(const mla_dims* dims, int max_blocks, mla_dims* d) {
 
 namespace {
 
-// The staged prefill: keys as bf16 tiles in the workspace, then blocks of 128 query rows.
+// Which keys the rows of a staged call see (chunk.h), and what says so.
+struct Span {
+  int kind = mla::kCausal;
+  int window = 0, sinks = 0;                                  // kWindow
+  const int32_t *group_indptr = nullptr, *prefix_indptr = nullptr, *prefix_indices = nullptr;  // kShared
+  int groups = 0, num_prefix = 0;
+};
+
+// dims of a staged call, `decode`: without qo_indptr, a token per request.
+int check_span(const mla_dims* dims, bool decode, const Span& span, mla_dims* d) {
+  const int st = check_dims(dims, !decode);
+  if (st != MLA_OK) return st;
+  *d = *dims;
+  if (decode) d->total_q = d->batch;
+  if (span.kind == mla::kWindow && (span.window < 1 || span.sinks < 0)) return MLA_ERR_DIMS;
+  if (span.kind == mla::kShared && (span.groups < 0 || span.num_prefix < 0)) return MLA_ERR_DIMS;
+  return MLA_OK;
+}
+
+// The workspace of a staged call.  kWindow: tiles for all keys, or only for those that a request's
+// tokens see, whichever are fewer (per_request > 0: the latter).
+mla::ChunkLayout staged_layout(const mla_dims& d, const Span& span, int workers, int* per_request, int* prefix_tiles) {
+  *per_request = *prefix_tiles = 0;
+  if (span.kind == mla::kCausal)
+    return mla::ChunkLayout(workers, d.num_qo_heads, d.batch, d.total_q, d.num_kv_indices);
+  auto tiles_of = [](long long keys) { return (keys + mla::kChunkKeys - 1) / mla::kChunkKeys; };
+  long long tiles = tiles_of(d.num_kv_indices) + d.batch;
+  if (span.kind == mla::kWindow) {
+    const long long per = mla::window_tiles_per_request(span.window, span.sinks);
+    const long long seen = d.batch * per + tiles_of(d.total_q);
+    if (seen < tiles) {
+      tiles = seen;
+      *per_request = (int)per;
+    }
+    return mla::ChunkLayout(workers, d.num_qo_heads, d.batch, d.total_q, tiles, 0);
+  }
+  const long long prefixes = tiles_of(span.num_prefix) + span.groups;
+  *prefix_tiles = (int)(prefixes < (1LL << 30) ? prefixes : 1LL << 30);  // (more is refused: not addressable)
+  return mla::ChunkLayout(workers, d.num_qo_heads, span.groups, d.total_q, prefixes + tiles, d.batch);
+}
+
+size_t staged_workspace(const mla_dims* dims, bool decode, const Span& span) {
+  mla_dims d;
+  int G = 0, per = 0, prefixes = 0;
+  if (check_span(dims, decode, span, &d) != MLA_OK || resolve_workers(&d, &G) != MLA_OK) return 0;
+  const mla::ChunkLayout lay = staged_layout(d, span, G, &per, &prefixes);
+  return lay.addressable() ? lay.total : 0;
+}
+
+// The staged attention: keys as bf16 tiles in the workspace, then blocks of 128 query rows.
 int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache, const void* kv_fp8,
                bool fp8, const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale,
-               void* out, float* lse, const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags,
-               void* stream_ptr) {
-  int st = check_dims(dims, true);
+               void* out, float* lse, const mla_dims* call_dims, void* workspace, size_t workspace_bytes, int flags,
+               void* stream_ptr, bool decode = false, const Span& span = Span{}) {
+  mla_dims resolved{};
+  int st = check_span(call_dims, decode, span, &resolved);
   if (st != MLA_OK) return st;
+  const mla_dims* dims = &resolved;
   if (!std::isfinite(sm_scale)) return MLA_ERR_DIMS;
   if (dims->total_q == 0 || dims->batch == 0) return MLA_OK;
-  if (!q_nope || !q_pe || !qo_indptr || !kv_indptr || !out || !lse) return MLA_ERR_NULL;
+  if (span.kind == mla::kShared && span.groups == 0) return MLA_OK;  // (no request is in a group)
+  if (!q_nope || !q_pe || (!decode && !qo_indptr) || !kv_indptr || !out || !lse) return MLA_ERR_NULL;
+  if (span.kind == mla::kShared && (!span.group_indptr || !span.prefix_indptr)) return MLA_ERR_NULL;
+  if (span.num_prefix > 0 && !span.prefix_indices) return MLA_ERR_NULL;
   if (dims->num_kv_indices > 0 && !kv_indices) return MLA_ERR_NULL;
   if (dims->num_pages > 0 && (fp8 ? !kv_fp8 : !ckv_cache || !kpe_cache)) return MLA_ERR_NULL;
   if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(ckv_cache) || !aligned16(kpe_cache) || !aligned16(kv_fp8) ||
       !aligned16(out))
     return MLA_ERR_ALIGN;
-  int G = 0;
+  int G = 0, per_request = 0, prefix_tiles = 0;
   if ((st = resolve_workers(dims, &G)) != MLA_OK) return st;
-  const mla::ChunkLayout lay(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices);
+  const mla::ChunkLayout lay = staged_layout(*dims, span, G, &per_request, &prefix_tiles);
   if (!lay.addressable()) return MLA_ERR_DIMS;
   if (!workspace || workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return MLA_ERR_ALIGN;
@@ -461,8 +532,19 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
   p.kpe = reinterpret_cast<__nv_bfloat16*>(ws + lay.kpe);
   p.part_lse = reinterpret_cast<float*>(ws + lay.part_lse);
   p.part_o = reinterpret_cast<float*>(ws + lay.part_o);
+  p.own_tiles = reinterpret_cast<int32_t*>(ws + lay.own_tiles);
   p.tiles = (int)lay.tiles;
   p.max_blocks = (int)lay.max_blocks;
+  // (no request has more keys than there are indices)
+  p.window = span.window < dims->num_kv_indices ? span.window : dims->num_kv_indices;
+  p.sinks = span.sinks < dims->num_kv_indices ? span.sinks : dims->num_kv_indices;
+  p.per_request = per_request;
+  p.group_indptr = span.group_indptr;
+  p.prefix_indptr = span.prefix_indptr;
+  p.prefix_indices = span.prefix_indices;
+  p.groups = span.groups;
+  p.num_prefix = span.num_prefix;
+  p.prefix_tiles = prefix_tiles;
   p.wait_ns = g_wait_ns.load();
   p.fault_skip_tile = g_fault_skip_tile.load();
 
@@ -488,14 +570,16 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
     v.num_kv_indices = dims->num_kv_indices;
     v.status = p.status;
     if (mla::launch_validate(v, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
+    if (span.kind == mla::kShared && mla::launch_validate_groups(p, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
   }
   // Benchmark timing, as in run(): staging and attention, then the merge.
   std::unique_lock<std::mutex> prof_lk(g_prof_mu);
   cudaEvent_t* ev = profile_slot();
   if (!ev) prof_lk.unlock();
   if (ev) cudaEventRecord(ev[0], stream);
-  if (mla::launch_chunk_stage(p, fp8, stream) != cudaSuccess || mla::launch_chunk(maps, p, stream) != cudaSuccess)
-    return MLA_ERR_LAUNCH;
+  const cudaError_t staged = span.kind == mla::kCausal ? mla::launch_chunk_stage(p, fp8, stream)
+                                                       : mla::launch_span_stage(p, span.kind, fp8, stream);
+  if (staged != cudaSuccess || mla::launch_chunk(maps, p, span.kind, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
   if (ev) cudaEventRecord(ev[1], stream);
   if (mla::launch_chunk_merge(p, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
   if (ev) cudaEventRecord(ev[2], stream);
@@ -506,13 +590,7 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
 
 extern "C" {
 
-size_t mla_workspace_bytes_prefill_staged(const mla_dims* dims) {
-  if (check_dims(dims, true) != MLA_OK) return 0;
-  int G = 0;
-  if (resolve_workers(dims, &G) != MLA_OK) return 0;
-  const mla::ChunkLayout lay(G, dims->num_qo_heads, dims->batch, dims->total_q, dims->num_kv_indices);
-  return lay.addressable() ? lay.total : 0;
-}
+size_t mla_workspace_bytes_prefill_staged(const mla_dims* dims) { return staged_workspace(dims, false, Span{}); }
 
 int mla_paged_prefill_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
                              const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices,
@@ -529,6 +607,114 @@ int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_f
                           const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream) {
   return run_staged(q_nope, q_pe, nullptr, nullptr, kv_fp8, true, qo_indptr, kv_indptr, kv_indices, sm_scale, out, lse,
                     dims, workspace, workspace_bytes, flags, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+Span window_span(int window, int sinks) {
+  Span s;
+  s.kind = mla::kWindow;
+  s.window = window;
+  s.sinks = sinks;
+  return s;
+}
+
+Span shared_span(const int32_t* group_indptr, int groups, const int32_t* prefix_indptr, const int32_t* prefix_indices,
+                 int num_prefix_indices) {
+  Span s;
+  s.kind = mla::kShared;
+  s.group_indptr = group_indptr;
+  s.prefix_indptr = prefix_indptr;
+  s.prefix_indices = prefix_indices;
+  s.groups = groups;
+  s.num_prefix = num_prefix_indices;
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mla_workspace_bytes_window(const mla_dims* dims, int window, int sinks, int is_prefill) {
+  return staged_workspace(dims, !is_prefill, window_span(window, sinks));
+}
+
+int mla_paged_decode_window(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                            const int32_t* kv_indptr, const int32_t* kv_indices, int window, int sinks, float sm_scale,
+                            void* out, float* lse, const mla_dims* dims, void* workspace, size_t workspace_bytes,
+                            int flags, void* stream) {
+  return run_staged(q_nope, q_pe, ckv_cache, kpe_cache, nullptr, false, nullptr, kv_indptr, kv_indices, sm_scale, out,
+                    lse, dims, workspace, workspace_bytes, flags, stream, true, window_span(window, sinks));
+}
+
+int mla_paged_decode_window_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* kv_indptr,
+                                const int32_t* kv_indices, int window, int sinks, float sm_scale, void* out, float* lse,
+                                const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags,
+                                void* stream) {
+  return run_staged(q_nope, q_pe, nullptr, nullptr, kv_fp8, true, nullptr, kv_indptr, kv_indices, sm_scale, out, lse,
+                    dims, workspace, workspace_bytes, flags, stream, true, window_span(window, sinks));
+}
+
+int mla_paged_prefill_window(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                             const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices, int window,
+                             int sinks, float sm_scale, void* out, float* lse, const mla_dims* dims, void* workspace,
+                             size_t workspace_bytes, int flags, void* stream) {
+  return run_staged(q_nope, q_pe, ckv_cache, kpe_cache, nullptr, false, qo_indptr, kv_indptr, kv_indices, sm_scale, out,
+                    lse, dims, workspace, workspace_bytes, flags, stream, false, window_span(window, sinks));
+}
+
+int mla_paged_prefill_window_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
+                                 const int32_t* kv_indptr, const int32_t* kv_indices, int window, int sinks,
+                                 float sm_scale, void* out, float* lse, const mla_dims* dims, void* workspace,
+                                 size_t workspace_bytes, int flags, void* stream) {
+  return run_staged(q_nope, q_pe, nullptr, nullptr, kv_fp8, true, qo_indptr, kv_indptr, kv_indices, sm_scale, out, lse,
+                    dims, workspace, workspace_bytes, flags, stream, false, window_span(window, sinks));
+}
+
+size_t mla_workspace_bytes_shared(const mla_dims* dims, int groups, int num_prefix_indices, int is_prefill) {
+  return staged_workspace(dims, !is_prefill, shared_span(nullptr, groups, nullptr, nullptr, num_prefix_indices));
+}
+
+int mla_paged_decode_shared(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                            const int32_t* group_indptr, int groups, const int32_t* prefix_indptr,
+                            const int32_t* prefix_indices, int num_prefix_indices, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, float sm_scale, void* out, float* lse, const mla_dims* dims,
+                            void* workspace, size_t workspace_bytes, int flags, void* stream) {
+  return run_staged(q_nope, q_pe, ckv_cache, kpe_cache, nullptr, false, nullptr, kv_indptr, kv_indices, sm_scale, out,
+                    lse, dims, workspace, workspace_bytes, flags, stream, true,
+                    shared_span(group_indptr, groups, prefix_indptr, prefix_indices, num_prefix_indices));
+}
+
+int mla_paged_decode_shared_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* group_indptr,
+                                int groups, const int32_t* prefix_indptr, const int32_t* prefix_indices,
+                                int num_prefix_indices, const int32_t* kv_indptr, const int32_t* kv_indices,
+                                float sm_scale, void* out, float* lse, const mla_dims* dims, void* workspace,
+                                size_t workspace_bytes, int flags, void* stream) {
+  return run_staged(q_nope, q_pe, nullptr, nullptr, kv_fp8, true, nullptr, kv_indptr, kv_indices, sm_scale, out, lse,
+                    dims, workspace, workspace_bytes, flags, stream, true,
+                    shared_span(group_indptr, groups, prefix_indptr, prefix_indices, num_prefix_indices));
+}
+
+int mla_paged_prefill_shared(const void* q_nope, const void* q_pe, const void* ckv_cache, const void* kpe_cache,
+                             const int32_t* qo_indptr, const int32_t* group_indptr, int groups,
+                             const int32_t* prefix_indptr, const int32_t* prefix_indices, int num_prefix_indices,
+                             const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out, float* lse,
+                             const mla_dims* dims, void* workspace, size_t workspace_bytes, int flags, void* stream) {
+  return run_staged(q_nope, q_pe, ckv_cache, kpe_cache, nullptr, false, qo_indptr, kv_indptr, kv_indices, sm_scale, out,
+                    lse, dims, workspace, workspace_bytes, flags, stream, false,
+                    shared_span(group_indptr, groups, prefix_indptr, prefix_indices, num_prefix_indices));
+}
+
+int mla_paged_prefill_shared_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const int32_t* qo_indptr,
+                                 const int32_t* group_indptr, int groups, const int32_t* prefix_indptr,
+                                 const int32_t* prefix_indices, int num_prefix_indices, const int32_t* kv_indptr,
+                                 const int32_t* kv_indices, float sm_scale, void* out, float* lse, const mla_dims* dims,
+                                 void* workspace, size_t workspace_bytes, int flags, void* stream) {
+  return run_staged(q_nope, q_pe, nullptr, nullptr, kv_fp8, true, qo_indptr, kv_indptr, kv_indices, sm_scale, out, lse,
+                    dims, workspace, workspace_bytes, flags, stream, false,
+                    shared_span(group_indptr, groups, prefix_indptr, prefix_indices, num_prefix_indices));
 }
 
 }  // extern "C"

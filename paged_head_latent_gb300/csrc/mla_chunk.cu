@@ -176,6 +176,83 @@ struct Walk {
   }
 };
 
+// A walk that knows the staged tile it stands at, that tile's first key among its list's and,
+// for kShared, the request whose own keys it holds.
+template <int kSpan>
+struct TileWalk : Walk {
+  int tile, key0;
+  // kShared: the request (-1: the prefix), its tokens and keys, tiles left of them, and whether
+  // this is the first tile of theirs.
+  int req, q0, q_len, len, left;
+  bool fresh;
+  __device__ TileWalk(const ChunkParams& params, int w) : Walk(params, w) { place(); }
+  __device__ void place() {
+    if constexpr (kSpan == kCausal) {
+      tile = blk.tile0 + t;
+      key0 = t * kChunkKeys;
+    } else if constexpr (kSpan == kWindow) {
+      const int over = t - blk.head;
+      tile = over < 0 ? blk.tile0 + t : blk.rest0 + over;
+      key0 = (over < 0 ? t : blk.rest_key + over) * kChunkKeys;
+    } else if (live) {
+      if (t < blk.head) {
+        req = -1;
+        left = blk.head - t;
+        tile = blk.tile0 + t;
+        key0 = t * kChunkKeys;
+      } else {
+        int skip = t - blk.head;
+        req = blk.req - 1;
+        next_request();
+        while (skip >= left && req < p.batch - 1) {
+          skip -= left;
+          next_request();
+        }
+        skip = min(skip, max(left - 1, 0));  // (corrupt offsets could name more tiles than there are)
+        tile += skip;
+        key0 = skip * kChunkKeys;
+        left -= skip;
+      }
+      fresh = true;
+    }
+  }
+  // The first tile of the next request with keys of its own (of the last request, if none has).
+  __device__ void next_request() {
+    do {
+      req = min(req + 1, p.batch - 1);
+      auto at = [&](const int32_t* ptr, int i, int most) { return min(max(__ldg(ptr + i), 0), most); };
+      const int k0 = at(p.kv_indptr, req, p.num_kv_indices);
+      len = max(at(p.kv_indptr, req + 1, p.num_kv_indices), k0) - k0;
+      q0 = req;
+      q_len = 1;
+      if (p.qo_indptr) {
+        q0 = at(p.qo_indptr, req, p.total_q);
+        q_len = max(at(p.qo_indptr, req + 1, p.total_q), q0) - q0;
+      }
+      tile = p.prefix_tiles + (k0 + kChunkKeys - 1) / kChunkKeys + req;
+      left = q_len > 0 ? (len + kChunkKeys - 1) / kChunkKeys : 0;
+    } while (left == 0 && req < p.batch - 1);
+    key0 = 0;
+    fresh = true;
+  }
+  __device__ void advance() {
+    Walk::advance();
+    if constexpr (kSpan != kShared) {
+      place();
+    } else if (first()) {
+      place();
+    } else if (--left > 0) {
+      ++tile;
+      key0 += kChunkKeys;
+      fresh = false;
+    } else {
+      if (req < 0) req = blk.req - 1;
+      next_request();
+    }
+  }
+};
+
+template <int kSpan>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -220,8 +297,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool fault = is_k && p.fault_skip_tile >= 1 && w == 0 && rank == 0;
       bool ok = true;
       uint32_t j = 0;
-      for (Walk it(p, w); it.live && ok; it.advance(), ++j) {
-        const int row = (it.blk.tile0 + it.t) * kChunkKeys;
+      for (TileWalk<kSpan> it(p, w); it.live && ok; it.advance(), ++j) {
+        const int row = it.tile * kChunkKeys;
         const uint32_t again = (j - 1) & 1;  // phase of the previous use of a buffer
         if (is_k) {
           if (fault && (int)j == p.fault_skip_tile) break;  // (test of the give-up path: no more loads)
@@ -339,7 +416,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t p_full = leader(P_FULL), o_empty = leader(O_EMPTY);
     const float scale = p.scale_log2;
     float m_ref = 0.f, l = 0.f;
-    int seen = 0;  // keys that this row sees
+    int seen = 0;  // keys that this row sees (kShared: of the prefix, or of the tile's request)
+    int token = 0;  // kShared: the row's token
     // The whole warp waits, and leaves together.
     auto wait = [&](uint32_t i, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort, p.status, kStatusTimeout, p.wait_ns));
@@ -347,11 +425,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort != 0); };
     bool ok = true;
     uint32_t j = 0;
-    for (Walk it(p, w); it.live; it.advance(), ++j) {
+    for (TileWalk<kSpan> it(p, w); it.live; it.advance(), ++j) {
       const bool first = it.first();
-      const int local = it.blk.local0 + 64 * rank + r;  // row within its request
-      if (first) seen = it.blk.seen + local / p.heads;
-      const uint32_t* fl = p.flags + (size_t)(it.blk.tile0 + it.t) * 8 + quarter;
+      if constexpr (kSpan == kShared) {
+        if (first) token = (it.blk.row0 + 64 * (int)rank + r) / p.heads;
+        if (it.fresh) {
+          const int nth = token - it.q0;  // the row's token among the request's
+          seen = it.req < 0 ? it.blk.seen : nth >= 0 && nth < it.q_len ? max(it.len - it.q_len + 1 + nth, 0) : 0;
+        }
+      } else {
+        const int local = it.blk.local0 + 64 * rank + r;  // row within its request
+        if (first) seen = it.blk.seen + local / p.heads;
+        if (kSpan == kWindow && first) seen = max(seen, 0);
+      }
+      const uint32_t* fl = p.flags + (size_t)it.tile * 8 + quarter;
       // (from L2: this kernel may have begun before the staging pass wrote them)
       const uint32_t keys = __ldcg(fl), odd = __ldcg(fl + 4);
       if (!wait(S_FULL + (j & 1), (j >> 1) & 1)) {
@@ -365,10 +452,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float s[32];
 #pragma unroll
       for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(raw[k]);
-      const int n = seen - it.t * kChunkKeys - 32 * quarter;  // keys of this thread's part that the row sees
-      const bool full = n >= 32 && keys == 0xffffffffu && odd == 0 && scale >= 0.f;
+      const int n = seen - it.key0 - 32 * quarter;  // keys of this thread's part that the row sees
+      auto below = [](int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u; };
+      uint32_t hidden = 0;  // kWindow: keys in front of the window that are no sinks
+      if constexpr (kSpan == kWindow)
+        hidden = n > p.window ? below(n - p.window) & ~below(p.sinks - it.key0 - 32 * quarter) : 0u;
+      const bool full = n >= 32 && keys == 0xffffffffu && odd == 0 && scale >= 0.f && hidden == 0;
       if (!full) {
-        const uint32_t see = keys & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
+        const uint32_t see = keys & below(n) & ~hidden;
         // (a staged key that is not finite is all zeros: its scores are finite, the row is NaN below)
         if (odd & see) l = __int_as_float(0x7fc00000);
 #pragma unroll
@@ -557,9 +648,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-}  // namespace
-
-cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, cudaStream_t stream) {
+template <int kSpan>
+cudaError_t launch_instance(const ChunkMaps& maps, const ChunkParams& p, cudaStream_t stream) {
   // The shared-memory attribute is set once per device; calls may come from any host thread.
   static std::mutex mu;
   static bool configured[64] = {};
@@ -568,7 +658,8 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, cudaStream
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!configured[dev]) {
-      const cudaError_t e = cudaFuncSetAttribute(chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+      const cudaError_t e =
+          cudaFuncSetAttribute(chunk_kernel<kSpan>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
       if (e != cudaSuccess) return e;
       configured[dev] = true;
     }
@@ -584,8 +675,16 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel, maps, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<kSpan>, maps, p);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, int span, cudaStream_t stream) {
+  return span == kWindow   ? launch_instance<kWindow>(maps, p, stream)
+         : span == kShared ? launch_instance<kShared>(maps, p, stream)
+                           : launch_instance<kCausal>(maps, p, stream);
 }
 
 }  // namespace mla

@@ -462,9 +462,11 @@ mla::ChunkLayout staged_layout(const mla_dims& d, const Span& span, int workers,
     }
     return mla::ChunkLayout(workers, d.num_qo_heads, d.batch, d.total_q, tiles, 0);
   }
+  // Prefixes in tiles, own keys in halves (of n keys at most n / 64 + 1), a half of zeros.
   const long long prefixes = tiles_of(span.num_prefix) + span.groups;
+  const long long halves = d.num_kv_indices / mla::kHalfKeys + (long long)d.batch + 1;
   *prefix_tiles = (int)(prefixes < (1LL << 30) ? prefixes : 1LL << 30);  // (more is refused: not addressable)
-  return mla::ChunkLayout(workers, d.num_qo_heads, span.groups, d.total_q, prefixes + tiles, d.batch);
+  return mla::ChunkLayout(workers, d.num_qo_heads, span.groups, d.total_q, prefixes + (halves + 1) / 2, d.batch);
 }
 
 size_t staged_workspace(const mla_dims* dims, bool decode, const Span& span) {
@@ -532,7 +534,7 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
   p.kpe = reinterpret_cast<__nv_bfloat16*>(ws + lay.kpe);
   p.part_lse = reinterpret_cast<float*>(ws + lay.part_lse);
   p.part_o = reinterpret_cast<float*>(ws + lay.part_o);
-  p.own_tiles = reinterpret_cast<int32_t*>(ws + lay.own_tiles);
+  p.own_halves = reinterpret_cast<int32_t*>(ws + lay.own_halves);
   p.tiles = (int)lay.tiles;
   p.max_blocks = (int)lay.max_blocks;
   // (no request has more keys than there are indices)
@@ -545,6 +547,14 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
   p.groups = span.groups;
   p.num_prefix = span.num_prefix;
   p.prefix_tiles = prefix_tiles;
+  p.infos = reinterpret_cast<mla::HalfInfo*>(ws + lay.infos);
+  p.zero_row = (int)(lay.tiles * mla::kChunkKeys - mla::kHalfKeys);
+  // Whole pages of 64 keys or more are read where they lie, if the rows that read them all see all
+  // of them (mla_span_stage.cu); a window's chunks have too few such keys.
+  const bool direct = !fp8 && dims->page_size % mla::kHalfKeys == 0 && p.num_slots > 0 &&
+                      (span.kind == mla::kShared || (span.kind == mla::kWindow && decode));
+  p.sources = direct ? reinterpret_cast<int32_t*>(ws + lay.sources) : nullptr;
+  p.aligned = direct || per_request == 0;
   p.wait_ns = g_wait_ns.load();
   p.fault_skip_tile = g_fault_skip_tile.load();
 
@@ -556,6 +566,11 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
   if ((st = get_map(&maps.q_pe, q_pe, rows, 64, 64, 64, sw, l128)) != MLA_OK) return st;
   if ((st = get_map(&maps.ckv, p.ckv, keys, 512, 64, 64, sw, l256)) != MLA_OK) return st;
   if ((st = get_map(&maps.kpe, p.kpe, keys, 64, 64, 64, sw, l128)) != MLA_OK) return st;
+  if (p.sources) {
+    const uint64_t slots = (uint64_t)p.num_slots;
+    if ((st = get_map(&maps.cache_ckv, ckv_cache, slots, 512, 64, 64, sw, l256)) != MLA_OK) return st;
+    if ((st = get_map(&maps.cache_kpe, kpe_cache, slots, 64, 64, 64, sw, l128)) != MLA_OK) return st;
+  }
 
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   cudaGetLastError();  // clear stale errors so the checks below see only ours

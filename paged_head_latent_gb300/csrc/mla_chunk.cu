@@ -176,83 +176,19 @@ struct Walk {
   }
 };
 
-// A walk that knows the staged tile it stands at, that tile's first key among its list's and,
-// for kShared, the request whose own keys it holds.
+// ---- the window and the shared attention: a tile's two halves of 64 keys
+// Staged row of half h of the tile that a walk stands at (of an odd block's last tile: of a half that
+// may be loaded).
 template <int kSpan>
-struct TileWalk : Walk {
-  int tile, key0;
-  // kShared: the request (-1: the prefix), its tokens and keys, tiles left of them, and whether
-  // this is the first tile of theirs.
-  int req, q0, q_len, len, left;
-  bool fresh;
-  __device__ TileWalk(const ChunkParams& params, int w) : Walk(params, w) { place(); }
-  __device__ void place() {
-    if constexpr (kSpan == kCausal) {
-      tile = blk.tile0 + t;
-      key0 = t * kChunkKeys;
-    } else if constexpr (kSpan == kWindow) {
-      const int over = t - blk.head;
-      tile = over < 0 ? blk.tile0 + t : blk.rest0 + over;
-      key0 = (over < 0 ? t : blk.rest_key + over) * kChunkKeys;
-    } else if (live) {
-      if (t < blk.head) {
-        req = -1;
-        left = blk.head - t;
-        tile = blk.tile0 + t;
-        key0 = t * kChunkKeys;
-      } else {
-        int skip = t - blk.head;
-        req = blk.req - 1;
-        next_request();
-        while (skip >= left && req < p.batch - 1) {
-          skip -= left;
-          next_request();
-        }
-        skip = min(skip, max(left - 1, 0));  // (corrupt offsets could name more tiles than there are)
-        tile += skip;
-        key0 = skip * kChunkKeys;
-        left -= skip;
-      }
-      fresh = true;
-    }
-  }
-  // The first tile of the next request with keys of its own (of the last request, if none has).
-  __device__ void next_request() {
-    do {
-      req = min(req + 1, p.batch - 1);
-      auto at = [&](const int32_t* ptr, int i, int most) { return min(max(__ldg(ptr + i), 0), most); };
-      const int k0 = at(p.kv_indptr, req, p.num_kv_indices);
-      len = max(at(p.kv_indptr, req + 1, p.num_kv_indices), k0) - k0;
-      q0 = req;
-      q_len = 1;
-      if (p.qo_indptr) {
-        q0 = at(p.qo_indptr, req, p.total_q);
-        q_len = max(at(p.qo_indptr, req + 1, p.total_q), q0) - q0;
-      }
-      tile = p.prefix_tiles + (k0 + kChunkKeys - 1) / kChunkKeys + req;
-      left = q_len > 0 ? (len + kChunkKeys - 1) / kChunkKeys : 0;
-    } while (left == 0 && req < p.batch - 1);
-    key0 = 0;
-    fresh = true;
-  }
-  __device__ void advance() {
-    Walk::advance();
-    if constexpr (kSpan != kShared) {
-      place();
-    } else if (first()) {
-      place();
-    } else if (--left > 0) {
-      ++tile;
-      key0 += kChunkKeys;
-      fresh = false;
-    } else {
-      if (req < 0) req = blk.req - 1;
-      next_request();
-    }
-  }
-};
+__device__ __forceinline__ int half_row(const ChunkParams& p, const Walk& it, int h) {
+  int u = 2 * it.t + h;
+  if (kSpan == kShared && u >= it.blk.halves) return p.zero_row;
+  if (kSpan == kWindow) u = max(min(u, it.blk.halves - 1), 0);
+  return u < it.blk.head ? it.blk.tile0 + kHalfKeys * u : it.blk.rest0 + kHalfKeys * (u - it.blk.head);
+}
 
-template <int kSpan>
+// kDirect: p.sources says which halves are read from the caches.
+template <int kSpan, bool kDirect>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -297,8 +233,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool fault = is_k && p.fault_skip_tile >= 1 && w == 0 && rank == 0;
       bool ok = true;
       uint32_t j = 0;
-      for (TileWalk<kSpan> it(p, w); it.live && ok; it.advance(), ++j) {
-        const int row = it.tile * kChunkKeys;
+      // The staged rows of a tile's halves; or the cache slots, which are read a tile ahead.
+      int rows[2], slots[2] = {-1, -1};
+      Walk ahead(p, w);
+      auto look = [&]() {
+        if (!ahead.live) return;
+        if constexpr (kSpan == kCausal) {
+          rows[0] = (ahead.blk.tile0 + ahead.t) * kChunkKeys;
+          rows[1] = rows[0] + kHalfKeys;
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            rows[h] = half_row<kSpan>(p, ahead, h);
+            if (kDirect) slots[h] = __ldcg(p.sources + rows[h] / kHalfKeys);
+          }
+        }
+      };
+      look();
+      for (; ahead.live && ok; ++j) {
+        const bool first = ahead.first();
+        const int q_row = ahead.blk.row0, row[2] = {rows[0], rows[1]}, slot[2] = {slots[0], slots[1]};
+        ahead.advance();
+        look();
+        auto load = [&](uint32_t dst, int c, uint32_t h, uint32_t to) {  // columns 64 c .. of half h's keys
+          const bool cached = kDirect && (h ? slot[1] : slot[0]) >= 0;
+          const CUtensorMap* map = c < 8 ? (cached ? &maps.cache_ckv : &maps.ckv) : (cached ? &maps.cache_kpe : &maps.kpe);
+          tma_load_pair(dst, map, c < 8 ? 64 * c : 0, cached ? (h ? slot[1] : slot[0]) : h ? row[1] : row[0], to);
+        };
         const uint32_t again = (j - 1) & 1;  // phase of the previous use of a buffer
         if (is_k) {
           if (fault && (int)j == p.fault_skip_tile) break;  // (test of the give-up path: no more loads)
@@ -311,14 +272,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(bar(K_FULL + g), 2 * kGroup * kBox);
 #pragma unroll
             for (int c = kGroup * g; c < (int)(kGroup * (g + 1)); ++c)
-              tma_load_pair(base + kOffK + c * kBox, c < 8 ? &maps.ckv : &maps.kpe, c < 8 ? 64 * c : 0, row + 64 * rank,
-                            leader(K_FULL + g));
+              load(base + kOffK + c * kBox, c, rank, leader(K_FULL + g));
           }
-          if (it.first() && ok) {  // (the previous block's last S is done, so Q is free)
+          if (first && ok) {  // (the previous block's last S is done, so Q is free)
             if (rank == 0) mbar_arrive_expect_tx(bar(Q_FULL), 2 * kKBoxes * kBox);
             for (int c = 0; c < kKBoxes; ++c)
               tma_load_pair(base + kOffQ + c * kBox, c < 8 ? &maps.q_nope : &maps.q_pe, c < 8 ? 64 * c : 0,
-                            it.blk.row0 + 64 * rank, leader(Q_FULL));
+                            q_row + 64 * rank, leader(Q_FULL));
           }
         } else {
 #pragma unroll
@@ -328,8 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(bar(V_FULL + h), 8 * kBox);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              tma_load_pair(base + kOffV + (4 * h + c) * kBox, &maps.ckv, 256 * rank + 64 * c, row + 64 * h,
-                            leader(V_FULL + h));
+              load(base + kOffV + (4 * h + c) * kBox, 4 * (int)rank + c, h, leader(V_FULL + h));
           }
         }
       }
@@ -416,31 +375,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t p_full = leader(P_FULL), o_empty = leader(O_EMPTY);
     const float scale = p.scale_log2;
     float m_ref = 0.f, l = 0.f;
-    int seen = 0;  // keys that this row sees (kShared: of the prefix, or of the tile's request)
-    int token = 0;  // kShared: the row's token
+    int seen = 0;   // keys that this row sees (kCausal)
+    int token = 0;  // the row's token (kWindow: of its request)
     // The whole warp waits, and leaves together.
     auto wait = [&](uint32_t i, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort, p.status, kStatusTimeout, p.wait_ns));
     };
     auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort != 0); };
+    auto below = [](int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u; };
+    // kWindow, kShared: which of the next tile's keys the row sees, asked for a tile ahead, as each
+    // instruction and each load between a tile's scores and its weights counts.
+    struct {
+      int row, u, slot;
+      uint32_t keys[2], odd[2];
+      int4 info;
+    } next;
+    Walk ahead(p, w);
+    auto look = [&]() {
+      if constexpr (kSpan != kCausal) {
+        if (!ahead.live) return;
+        next.u = 2 * ahead.t + half;
+        const int row = half_row<kSpan>(p, ahead, half), at = row + 32 * part;
+        next.row = row;
+        // (from L2: this kernel may have begun before the staging pass wrote them)
+        const uint32_t* fl = p.flags + (at >> 5);
+        const size_t to_odd = (size_t)p.tiles * 4;
+        next.keys[0] = __ldcg(fl), next.odd[0] = __ldcg(fl + to_odd);
+        if (kSpan == kWindow && !kDirect && (at & 31)) next.keys[1] = __ldcg(fl + 1), next.odd[1] = __ldcg(fl + to_odd + 1);
+        if constexpr (kDirect) next.slot = __ldcg(p.sources + row / kHalfKeys);
+        if constexpr (kSpan == kShared) next.info = __ldcg(reinterpret_cast<const int4*>(p.infos + row / kHalfKeys));
+      }
+    };
+    look();
     bool ok = true;
     uint32_t j = 0;
-    for (TileWalk<kSpan> it(p, w); it.live; it.advance(), ++j) {
+    for (Walk it(p, w); it.live; it.advance(), ++j) {
       const bool first = it.first();
-      if constexpr (kSpan == kShared) {
-        if (first) token = (it.blk.row0 + 64 * (int)rank + r) / p.heads;
-        if (it.fresh) {
-          const int nth = token - it.q0;  // the row's token among the request's
-          seen = it.req < 0 ? it.blk.seen : nth >= 0 && nth < it.q_len ? max(it.len - it.q_len + 1 + nth, 0) : 0;
-        }
-      } else {
+      uint32_t keys, odd;
+      int n;                // keys of this thread's part that the row sees
+      uint32_t hidden = 0;  // ... but for these
+      bool cached = false;  // all are keys then, but any may not be finite
+      if constexpr (kSpan == kCausal) {
         const int local = it.blk.local0 + 64 * rank + r;  // row within its request
         if (first) seen = it.blk.seen + local / p.heads;
-        if (kSpan == kWindow && first) seen = max(seen, 0);
+        n = seen - it.t * kChunkKeys - 32 * quarter;
+        const uint32_t* fl = p.flags + (size_t)(it.blk.tile0 + it.t) * 8 + quarter;
+        // (from L2: this kernel may have begun before the staging pass wrote them)
+        keys = __ldcg(fl), odd = __ldcg(fl + 4);
+      } else {
+        if (first) token = ((kSpan == kShared ? it.blk.row0 : it.blk.local0) + 64 * (int)rank + r) / p.heads;
+        keys = next.keys[0], odd = next.odd[0];
+        if constexpr (kSpan == kShared) {
+          n = token >= next.info.x && token < next.info.y ? token + next.info.z - 32 * part : 0;
+        } else {
+          const int shift = next.row & 31, over = next.u - it.blk.head;
+          if (!kDirect && shift) {
+            keys = __funnelshift_r(keys, next.keys[1], shift);
+            odd = __funnelshift_r(odd, next.odd[1], shift);
+          }
+          const int key = (over < 0 ? kHalfKeys * next.u : it.blk.rest_key + kHalfKeys * over) + 32 * part;
+          const int sinks = p.sinks - key;
+          if (over < 0) {
+            n = min(sinks, it.blk.rest_key - key);
+          } else {
+            n = it.blk.seen + token - key;
+            if (n > p.window) hidden = below(n - p.window) & ~below(sinks);
+          }
+          if (next.u >= it.blk.halves) n = 0;
+        }
+        if (kDirect) cached = next.slot >= 0;
+        if (cached) keys = 0xffffffffu, odd = 0;
       }
-      const uint32_t* fl = p.flags + (size_t)it.tile * 8 + quarter;
-      // (from L2: this kernel may have begun before the staging pass wrote them)
-      const uint32_t keys = __ldcg(fl), odd = __ldcg(fl + 4);
       if (!wait(S_FULL + (j & 1), (j >> 1) & 1)) {
         ok = false;
         break;
@@ -448,15 +453,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint32_t raw[32];
       tmem_ld32(col_s + 64 * (j & 1), raw);
+      if constexpr (kSpan != kCausal) {
+        ahead.advance();
+        look();
+      }
       tmem_ld_wait();
       float s[32];
 #pragma unroll
       for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(raw[k]);
-      const int n = seen - it.key0 - 32 * quarter;  // keys of this thread's part that the row sees
-      auto below = [](int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u; };
-      uint32_t hidden = 0;  // kWindow: keys in front of the window that are no sinks
-      if constexpr (kSpan == kWindow)
-        hidden = n > p.window ? below(n - p.window) & ~below(p.sinks - it.key0 - 32 * quarter) : 0u;
+      if constexpr (kDirect) {
+        if (cached) {
+          // A key that is not finite makes a score that is not (an infinite weightless key would
+          // otherwise pass): the row is NaN, as with staged keys.
+          float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 32; ++k) z[k & 3] = fmaf(s[k], 0.f, z[k & 3]);
+          z[0] = (z[0] + z[1]) + (z[2] + z[3]);
+          if (z[0] != z[0]) l = z[0];
+        }
+      }
       const bool full = n >= 32 && keys == 0xffffffffu && odd == 0 && scale >= 0.f && hidden == 0;
       if (!full) {
         const uint32_t see = keys & below(n) & ~hidden;
@@ -648,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int kSpan>
+template <int kSpan, bool kDirect>
 cudaError_t launch_instance(const ChunkMaps& maps, const ChunkParams& p, cudaStream_t stream) {
   // The shared-memory attribute is set once per device; calls may come from any host thread.
   static std::mutex mu;
@@ -659,7 +674,7 @@ cudaError_t launch_instance(const ChunkMaps& maps, const ChunkParams& p, cudaStr
     std::lock_guard<std::mutex> lk(mu);
     if (!configured[dev]) {
       const cudaError_t e =
-          cudaFuncSetAttribute(chunk_kernel<kSpan>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+          cudaFuncSetAttribute(chunk_kernel<kSpan, kDirect>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
       if (e != cudaSuccess) return e;
       configured[dev] = true;
     }
@@ -675,16 +690,17 @@ cudaError_t launch_instance(const ChunkMaps& maps, const ChunkParams& p, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<kSpan>, maps, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<kSpan, kDirect>, maps, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, int span, cudaStream_t stream) {
-  return span == kWindow   ? launch_instance<kWindow>(maps, p, stream)
-         : span == kShared ? launch_instance<kShared>(maps, p, stream)
-                           : launch_instance<kCausal>(maps, p, stream);
+  const bool direct = p.sources != nullptr;
+  if (span == kWindow) return direct ? launch_instance<kWindow, true>(maps, p, stream) : launch_instance<kWindow, false>(maps, p, stream);
+  if (span == kShared) return direct ? launch_instance<kShared, true>(maps, p, stream) : launch_instance<kShared, false>(maps, p, stream);
+  return launch_instance<kCausal, false>(maps, p, stream);
 }
 
 }  // namespace mla

@@ -1,6 +1,11 @@
 // mla_span_stage.cu -- what runs before the window and the shared attention: their keys as
-// bf16 tiles of 128, and the plan.  (The attention is mla_chunk.cu's, the merge
-// mla_chunk_stage.cu's.)
+// bf16 rows, or where in the cache they are, and the plan.  (The attention is mla_chunk.cu's, the
+// merge mla_chunk_stage.cu's.)
+//
+// A block of 128 query rows walks halves of 64 keys, two to a tile.  A half is 64 consecutive rows,
+// staged ones or cache slots.  kShared: every list has halves of its own from its first key on.
+// kWindow: a block's halves are those of the sinks in front of its first row's window, and those
+// from that window's first key on (or, with p.aligned, from the multiple of 64 before it).
 #include "chunk.h"
 #include "ptx.cuh"
 
@@ -13,6 +18,7 @@ constexpr int kNear = 1024;     // entries of the plan's tables that are kept in
 constexpr int kBlockCost = 3;   // cost units (tiles) of starting a block, as in the staged prefill
 
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + kChunkKeys - 1) / kChunkKeys; }
+__device__ __forceinline__ int key_halves(int keys) { return (keys + kHalfKeys - 1) / kHalfKeys; }
 
 // Offsets are clamped, so corrupt ones lead to no access outside the buffers.
 __device__ __forceinline__ int clamped(const int32_t* ptr, int i, int most) { return min(max(__ldg(ptr + i), 0), most); }
@@ -35,27 +41,35 @@ __device__ __forceinline__ SpanReq load_request(const ChunkParams& p, int b) {
   return r;
 }
 
-// First staged tile of request b (kWindow: of its keys that any token sees), of group g's
+// kShared: halves of a request's own keys.
+__device__ __forceinline__ int own_halves(const SpanReq& r) { return r.q_len > 0 ? key_halves(r.kv_len) : 0; }
+// ... and room for all of them.
+__device__ __forceinline__ int own_room(const ChunkParams& p) { return (p.zero_row - p.prefix_tiles * kChunkKeys) / kHalfKeys; }
+
+// First staged tile of request b's keys (kWindow: of those that any of its tokens sees), of group g's
 // prefix.  As ceil(k1 / 128) - ceil(k0 / 128) + 1 >= ceil((k1 - k0) / 128), lists do not overlap.
 __device__ __forceinline__ int request_tile0(const ChunkParams& p, int b) {
   if (p.per_request) return b * p.per_request + key_tiles(p.qo_indptr ? clamped(p.qo_indptr, b, p.total_q) : b);
-  return p.prefix_tiles + key_tiles(clamped(p.kv_indptr, b, p.num_kv_indices)) + b;
+  return key_tiles(clamped(p.kv_indptr, b, p.num_kv_indices)) + b;
 }
 __device__ __forceinline__ int prefix_tile0(const ChunkParams& p, int g) {
   return key_tiles(clamped(p.prefix_indptr, g, p.num_prefix)) + g;
 }
 
-// kWindow: the key tiles of a request that its tokens see: the first `head`, and from `rest` on.
-struct SeenTiles {
-  int low;   // first key of the first token's window
-  int head, rest;
+// kWindow: the first key of the window of a token that sees `seen` keys (as halves begin there).
+__device__ __forceinline__ int window_key(const ChunkParams& p, int seen) {
+  const int low = max(0, max(seen, 0) - p.window);
+  return p.aligned ? low & ~(kHalfKeys - 1) : low;
+}
+// kWindow: how a request's keys are staged, from its first token's count of keys: `head` halves of
+// sinks, then the keys from `low` on; or, where sinks and window meet and in a layout with room for
+// all keys, the keys from 0 on.
+struct StagedKeys {
+  int head, low;
 };
-__device__ __forceinline__ SeenTiles seen_tiles(const ChunkParams& p, int seen_first, int seen_last) {
-  SeenTiles s;
-  s.low = max(0, max(seen_first, 0) - p.window);
-  s.rest = s.low / kChunkKeys;
-  s.head = min(key_tiles(min(p.sinks, max(seen_last, 0))), s.rest);
-  return s;
+__device__ __forceinline__ StagedKeys staged_keys(const ChunkParams& p, int seen) {
+  const int low = window_key(p, seen);
+  return low < p.sinks || !p.per_request ? StagedKeys{0, 0} : StagedKeys{key_halves(p.sinks), low};
 }
 
 // Exclusive sum over the block's threads.
@@ -106,22 +120,22 @@ __device__ void plan(const ChunkParams& p) {
   const Scan scan{part};
   const int lists = kSpan == kShared ? p.groups : p.batch;
   auto first_of = [&](int b) { return b < kNear ? near_first[b] : p.first_block[b]; };
-  auto own_before = [&](int b) { return b < kNear ? near_own[b] : p.own_tiles[b]; };
+  auto own_before = [&](int b) { return b < kNear ? near_own[b] : p.own_halves[b]; };
   auto cost_of = [&](int i) { return i < kNear ? near_cost[i] : p.blocks[i].cost0; };
   // The first token of request b (kShared: its place among the queries).
   auto token_of = [&](int b) { return p.qo_indptr ? clamped(p.qo_indptr, b, p.total_q) : b; };
   long long run = 0, total;
-  if constexpr (kSpan == kShared) {  // own tiles of the requests before each
+  if constexpr (kSpan == kShared) {  // own halves of the requests before each
     for (int base = 0; base < p.batch; base += kStageThreads) {
       const int b = base + threadIdx.x;
       int n = 0;
       if (b < p.batch) {
         const SpanReq r = load_request(p, b);
-        n = r.q_len > 0 ? key_tiles(r.kv_len) : 0;
+        n = own_halves(r);
       }
       const int at = (int)min(run + scan(n, &total), 0x7fffffffLL);
       if (b < kNear) near_own[b] = at;
-      else if (b < p.batch) p.own_tiles[b] = at;
+      else if (b < p.batch) p.own_halves[b] = at;
       run += total;
     }
     run = 0;
@@ -174,27 +188,24 @@ __device__ void plan(const ChunkParams& p) {
         const SpanReq r = load_request(p, hi);
         const int seen = min(r.kv_len, r.kv_len - r.q_len + 1 + t1 - r.q0);
         const int k0 = clamped(p.prefix_indptr, b, p.num_prefix);
-        blk.head = key_tiles(max(clamped(p.prefix_indptr, b + 1, p.num_prefix), k0) - k0);
-        blk.tile0 = prefix_tile0(p, b);
-        blk.req = lo;
-        blk.seen = 0x7fffffff;
-        blk.tiles = blk.head + max(0, own_before(hi) - own_before(lo)) + key_tiles(max(seen, 0));
-        if (blk.tiles == 0) {  // no row sees a key: the request's tile of zeros
-          blk.head = blk.tiles = 1;
-          blk.seen = 0;
-          blk.tile0 = request_tile0(p, lo);
-        }
+        blk.head = key_halves(max(clamped(p.prefix_indptr, b + 1, p.num_prefix), k0) - k0);
+        blk.tile0 = prefix_tile0(p, b) * kChunkKeys;
+        // (offsets that overlap could name more halves than there is room for)
+        const int before = min(own_before(lo), own_room(p)), own = max(0, own_before(hi) - own_before(lo));
+        blk.rest0 = p.prefix_tiles * kChunkKeys + before * kHalfKeys;
+        blk.halves = blk.head + min(own + min(key_halves(max(seen, 0)), own_halves(r)), own_room(p) - before);
       } else {
         const SpanReq r = load_request(p, b);
         blk.seen = r.kv_len - r.q_len + 1;
         const int first = blk.seen + blk.local0 / p.heads, last = blk.seen + (blk.local0 + blk.rows - 1) / p.heads;
-        const SeenTiles all = seen_tiles(p, blk.seen, r.kv_len), s = seen_tiles(p, first, last);
-        blk.tile0 = request_tile0(p, b);
-        blk.head = s.head;
-        blk.rest_key = s.rest;
-        blk.rest0 = blk.tile0 + (p.per_request ? all.head + s.rest - all.rest : s.rest);
-        blk.tiles = max(1, s.head + max(0, key_tiles(max(last, 0)) - s.rest));
+        const StagedKeys all = staged_keys(p, blk.seen);
+        blk.rest_key = window_key(p, first);
+        blk.head = key_halves(min(p.sinks, blk.rest_key));
+        blk.tile0 = request_tile0(p, b) * kChunkKeys;
+        blk.rest0 = blk.tile0 + all.head * kHalfKeys + blk.rest_key - all.low;
+        blk.halves = blk.head + key_halves(max(0, last - blk.rest_key));
       }
+      blk.tiles = max(1, (blk.halves + 1) / 2);
     }
     blk.cost0 = cost + scan(i < nblocks ? blk.tiles + kBlockCost : 0, &total);
     if (i < nblocks) {
@@ -229,11 +240,15 @@ __device__ void plan(const ChunkParams& p) {
   }
 }
 
-// Where a staged tile's keys come from: entries [from, from + kChunkKeys) of a list, of which
-// those in [low, end) and below `sinks` are keys that a row may see (numbers within the list).
-struct TileSource {
+// Where staged rows from a multiple of 32 on (and to the next multiple of 64) come from: entries
+// `from` .. of a list, of which those in [low, end) and those below `sinks` are keys that a row may see.
+struct RowSource {
   const int32_t* list;
   int from, low, sinks, end;
+  bool zero;    // the half of zeros: no list
+  bool direct;  // every row that reads this half of 64 keys sees all of them
+  HalfInfo info;  // kShared: of the half that begins here
+  __device__ bool holds(int key) const { return key < end && (key >= low || key < sinks); }
 };
 
 // The request or group that staged tile `tile` belongs to: the last one whose first tile is <= it
@@ -253,43 +268,208 @@ __device__ __forceinline__ int owner_of(int n, int tile, Tile0 tile0) {
   return lo;
 }
 
-// False if no block reads the tile.
-template <int kSpan>
-__device__ __forceinline__ bool tile_source(const ChunkParams& p, int tile, TileSource* s) {
-  if (kSpan == kShared && tile < p.prefix_tiles) {
-    const int g = owner_of(p.groups, tile, [&](int i) { return prefix_tile0(p, i); });
+// kShared: where every request's own halves begin.  Each block of threads makes the sums for itself,
+// for up to kNear runs of requests.
+struct OwnTable {
+  int before[kNear + 1];  // halves before a run; all of them behind the last
+  long long part[kStageThreads / 32];
+  __device__ static int run_length(int batch) { return (batch + kNear - 1) / kNear; }
+  __device__ void make(const ChunkParams& p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = run_length(p.batch);
+    constexpr int kRuns = kNear / kStageThreads;
+    long long n[kRuns], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      n[i] = sum;
+      const int run = threadIdx.x * kRuns + i;
+      for (int b = run * each; b < min((run + 1) * each, p.batch); ++b) sum += own_halves(load_request(p, b));
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    long long base = incl - sum;
+    for (int i = 0; i < warp; ++i) base += part[i];
+    // (offsets that overlap could name more halves than there is room for)
+    const long long room = own_room(p);
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) before[threadIdx.x * kRuns + i] = (int)min(base + n[i], room);
+    if (threadIdx.x == kStageThreads - 1) before[kNear] = (int)min(base + sum, room);
+    __syncthreads();
+  }
+  __device__ int total() const { return before[kNear]; }
+  // The request that own half x belongs to; x becomes the number of the half among the request's.
+  __device__ int find(const ChunkParams& p, int* x) const {
+    const int run = last_at_most(kNear, *x, [&](int i) { return before[i]; }), each = run_length(p.batch);
+    *x -= before[run];
+    int b = run * each;
+    for (; b < p.batch - 1; ++b) {
+      const int n = own_halves(load_request(p, b));
+      if (*x < n) break;
+      *x -= n;
+    }
+    return b;
+  }
+};
+
+// kShared: the source of rows of the prefixes' tiles, of the own halves or of the half of zeros.
+// False if no block reads these rows.
+__device__ __forceinline__ bool shared_source(const ChunkParams& p, const OwnTable& own, int row, RowSource* s) {
+  s->low = s->sinks = 0;
+  s->info = HalfInfo{0, 0, 0, 0};
+  s->zero = false;
+  const int prefix_rows = p.prefix_tiles * kChunkKeys;
+  if (row < prefix_rows) {
+    const int g = owner_of(p.groups, row / kChunkKeys, [&](int i) { return prefix_tile0(p, i); });
     const int k0 = clamped(p.prefix_indptr, g, p.num_prefix);
     s->list = p.prefix_indices + k0;
-    s->from = (tile - prefix_tile0(p, g)) * kChunkKeys;
-    s->low = s->sinks = 0;
+    s->from = row - prefix_tile0(p, g) * kChunkKeys;
     s->end = max(clamped(p.prefix_indptr, g + 1, p.num_prefix), k0) - k0;
-    return s->from >= 0 && s->from < s->end && clamped(p.group_indptr, g + 1, p.batch) > clamped(p.group_indptr, g, p.batch);
+    s->direct = true;  // (a block has rows of one group)
+    s->info = HalfInfo{0, kMany, kMany, 0};
+    return s->from >= 0 && s->from < key_halves(s->end) * kHalfKeys &&
+           clamped(p.group_indptr, g + 1, p.batch) > clamped(p.group_indptr, g, p.batch);
   }
-  const int b = owner_of(p.batch, tile, [&](int i) { return request_tile0(p, i); });
+  int at = (row - prefix_rows) / kHalfKeys;
+  if (at >= own.total()) {
+    s->zero = true;
+    s->from = s->end = 0;
+    s->direct = false;
+    return true;
+  }
+  const int b = own.find(p, &at);
   const SpanReq r = load_request(p, b);
-  const int at = tile - request_tile0(p, b);
-  if (at < 0 || r.q_len == 0) return false;
+  const int seen = r.kv_len - r.q_len + 1;  // keys that the first token sees
   s->list = p.kv_indices + r.k0;
   s->end = r.kv_len;
-  s->low = s->sinks = 0;
-  int key_tile = at;
-  if constexpr (kSpan == kWindow) {
-    const SeenTiles t = seen_tiles(p, r.kv_len - r.q_len + 1, r.kv_len);
-    if (p.per_request) key_tile = at < t.head ? at : at - t.head + t.rest;
-    else if (at >= t.head && at < t.rest) return false;
-    s->low = t.low;
-    s->sinks = p.sinks;
+  s->from = at * kHalfKeys + row % kHalfKeys;
+  s->info = HalfInfo{r.q0, r.q0 + r.q_len, seen - r.q0 - at * kHalfKeys, 0};
+  // A block may have rows of several requests, if it is not filled by a token.
+  s->direct = (at + 1) * kHalfKeys <= seen;
+  if (s->direct && p.sources && p.heads != kChunkRows) {
+    const int g = owner_of(p.groups, b, [&](int i) { return clamped(p.group_indptr, i, p.batch); });
+    s->direct = clamped(p.group_indptr, g + 1, p.batch) - clamped(p.group_indptr, g, p.batch) == 1;
   }
-  s->from = (int)min((long long)key_tile * kChunkKeys, 0x7fffff80LL);
-  // (a request without keys has one tile of zeros: its rows' weights are zero)
-  return s->from < s->end || at == 0;
+  return true;
 }
 
-// Block 0 makes the plan.  The others take parts of staged tiles: 32 keys of one list, read
-// through their slots, as the bf16 numbers that the cache holds or (kFp8) stands for.  Entries that
-// are no keys, slots outside the cache and keys with a value that is not finite are written as
-// zeros, so that a weight of zero always makes a zero product; the tile's flags tell which rows
-// are keys and which of them were not finite.
+// kWindow: the source of rows of a request's keys.  False if no block reads these rows.
+__device__ __forceinline__ bool window_source(const ChunkParams& p, int row, RowSource* s) {
+  const int b = owner_of(p.batch, row / kChunkKeys, [&](int i) { return request_tile0(p, i); });
+  const SpanReq r = load_request(p, b);
+  const int at = row - request_tile0(p, b) * kChunkKeys;
+  if (at < 0 || r.q_len == 0) return false;
+  const int seen = r.kv_len - r.q_len + 1;  // keys that the first token sees
+  s->list = p.kv_indices + r.k0;
+  s->end = r.kv_len;
+  s->from = at;
+  s->low = max(0, max(seen, 0) - p.window);
+  s->sinks = p.sinks;
+  s->direct = r.q_len == 1;  // (a block has rows of one request)
+  if (p.per_request) {
+    const StagedKeys k = staged_keys(p, seen);
+    if (at < k.head * kHalfKeys) return true;
+    s->from = min(at - k.head * kHalfKeys, 0x7fffffff - k.low) + k.low;
+    // (a half may start at any key and reach 63 rows past the last; without keys, one of zeros)
+    return s->from < s->end || s->from - s->end < kHalfKeys - 1;
+  }
+  const int half = at & ~(kHalfKeys - 1);  // (halves of this layout start at multiples of 64 keys)
+  if (half >= p.sinks && half + kHalfKeys <= s->low) return false;
+  return s->from < max(key_halves(s->end), 1) * kHalfKeys;
+}
+
+// The staged rows in use, 32 or 64 at a time (the lists may be shorter than their buffers).
+template <int kSpan>
+struct StagedRows {
+  int prefixes = 0, rows;  // rows in use, of the prefixes and in all
+  __device__ StagedRows(const ChunkParams& p, OwnTable* own) {
+    if constexpr (kSpan == kShared) {
+      own->make(p);
+      prefixes = min(p.prefix_tiles, key_tiles(clamped(p.prefix_indptr, p.groups, p.num_prefix)) + p.groups) * kChunkKeys;
+      rows = prefixes + (own->total() + 1) * kHalfKeys;
+    } else {
+      rows = min(p.tiles, request_tile0(p, p.batch)) * kChunkKeys;
+    }
+  }
+  // The staged row of the i-th row in use, and its source.
+  __device__ bool source(const ChunkParams& p, const OwnTable* own, int i, int* row, RowSource* s) const {
+    if constexpr (kSpan == kShared) {
+      *row = i < prefixes ? i : i - prefixes + p.prefix_tiles * kChunkKeys;
+      const bool used = shared_source(p, *own, *row, s);
+      if (s->zero) *row = p.zero_row + *row % kHalfKeys;
+      return used;
+    } else {
+      *row = i;
+      return window_source(p, i, s);
+    }
+  }
+};
+
+// Eight threads' worth of tokens at a time: the staged rows `row` .. + kTok - 1 of this warp, from
+// the cache's slots `mine` (lanes 0 .. kTok - 1; outside the cache: zeros).  Returns, to all lanes, the
+// rows that hold a value that is not finite (their values are written as zeros, so that a
+// weight of zero always makes a zero product).
+template <bool kFp8, int kTok>
+__device__ __forceinline__ uint32_t copy_tokens(const ChunkParams& p, size_t row, int mine) {
+  const int lane = threadIdx.x & 31;
+  // A lane has latent values 8 lane .. + 7 and 256 + 8 lane .. + 7, rope values 8 lane .. + 7.
+  uint4 lat[kTok][2], rope[kTok];
+  uint2 code[kTok][2];
+  float sc[kTok][2];
+#pragma unroll
+  for (int k = 0; k < kTok; ++k) {
+    const int slot = __shfl_sync(0xffffffffu, mine, k);
+    lat[k][0] = lat[k][1] = rope[k] = make_uint4(0, 0, 0, 0);
+    code[k][0] = code[k][1] = make_uint2(0, 0);
+    sc[k][0] = sc[k][1] = 0.f;
+    if (slot < 0 || slot >= p.num_slots) continue;
+    if constexpr (kFp8) {
+      const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        code[k][h] = *reinterpret_cast<const uint2*>(tok + 256 * h + 8 * lane);
+        sc[k][h] = *reinterpret_cast<const float*>(tok + kDimCkv + 8 * h + 4 * (lane >> 4));
+      }
+      if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
+    } else {
+      const uint4* tok = reinterpret_cast<const uint4*>(p.ckv_cache + (size_t)slot * kDimCkv);
+      lat[k][0] = tok[lane];
+      lat[k][1] = tok[32 + lane];
+      if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * lane);
+    }
+  }
+  uint32_t bad = 0;
+#pragma unroll
+  for (int k = 0; k < kTok; ++k) {
+    uint4 a = lat[k][0], b = lat[k][1];
+    if constexpr (kFp8) {
+      a = ptx::e4m3x8_scaled_to_bf16x8(code[k][0], sc[k][0]);
+      b = ptx::e4m3x8_scaled_to_bf16x8(code[k][1], sc[k][1]);
+    }
+    const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, rope[k].x, rope[k].y, rope[k].z, rope[k].w};
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < 12; ++i) odd |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);  // exponent all ones
+    if (__any_sync(0xffffffffu, odd != 0)) {
+      a = b = rope[k] = make_uint4(0, 0, 0, 0);
+      bad |= 1u << k;
+    }
+    uint4* dst = reinterpret_cast<uint4*>(p.ckv + (row + k) * kDimCkv);
+    dst[lane] = a;
+    dst[32 + lane] = b;
+    if (lane < 8) *reinterpret_cast<uint4*>(p.kpe + (row + k) * kDimKpe + 8 * lane) = rope[k];
+  }
+  return bad;
+}
+
+// Block 0 makes the plan.  The others take 32 staged rows at a time, of one list, read through
+// their slots as the bf16 numbers that the cache holds or (kFp8) stands for.  Entries that are no
+// keys and slots outside the cache are written as zeros; the flags tell which rows are keys and
+// which of them were not finite.
 template <bool kFp8, int kSpan>
 __global__ void __launch_bounds__(kStageThreads) span_stage_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -298,78 +478,101 @@ __global__ void __launch_bounds__(kStageThreads) span_stage_kernel(const ChunkPa
     return;
   }
   __shared__ uint32_t is_key, is_odd;
+  __shared__ OwnTable own;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kParts = kChunkKeys / kStageKeys;
-  // The lists may be shorter than their buffers: only the tiles in use are walked.
-  int prefixes = 0;
-  if constexpr (kSpan == kShared) prefixes = min(p.prefix_tiles, key_tiles(clamped(p.prefix_indptr, p.groups, p.num_prefix)) + p.groups);
-  const int used = min(p.tiles, request_tile0(p, p.batch)) - p.prefix_tiles + prefixes;
-  for (int at_part = blockIdx.x - 1; at_part < used * kParts; at_part += gridDim.x - 1) {
-    const int nth = at_part / kParts, first = at_part % kParts * kStageKeys;
-    const int tile = nth < prefixes ? nth : nth - prefixes + p.prefix_tiles;
-    TileSource src;
-    if (!tile_source<kSpan>(p, tile, &src)) continue;
-    constexpr int kTok = kStageKeys * 32 / kStageThreads;  // a warp's tokens, all in flight
-    const int k0 = first + warp * kTok;
+  constexpr int kTok = kStageKeys * 32 / kStageThreads;
+  const StagedRows<kSpan> staged(p, &own);
+  for (int part = blockIdx.x - 1; part < staged.rows / kStageKeys; part += gridDim.x - 1) {
+    int row;
+    RowSource src;
+    if (!staged.source(p, &own, part * kStageKeys, &row, &src)) continue;
     int mine = -1;
-    if (lane < kTok) {
-      const int key = src.from + k0 + lane;
-      if (key < src.end && (key >= src.low || key < src.sinks)) mine = __ldg(src.list + key);
-    }
+    const int key = src.from + warp * kTok + lane;
+    if (lane < kTok && src.holds(key)) mine = __ldg(src.list + key);
     __syncthreads();  // (the flags of the last round are written)
     if (threadIdx.x == 0) is_key = is_odd = 0;
     __syncthreads();
-    if (mine >= p.num_slots) mine = -1;
-    uint4 lat[kTok][kFp8 ? 1 : 2], rope[kTok];  // lane: latent values 16 lane .. + 15, rope values 8 lane .. + 7
-    float sc[kTok];
-#pragma unroll
-    for (int k = 0; k < kTok; ++k) {
-      const int slot = __shfl_sync(0xffffffffu, mine, k);
-      lat[k][0] = lat[k][kFp8 ? 0 : 1] = rope[k] = make_uint4(0, 0, 0, 0);
-      sc[k] = 0.f;
-      if (slot < 0) continue;
-      if constexpr (kFp8) {
-        const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
-        lat[k][0] = *reinterpret_cast<const uint4*>(tok + 16 * lane);
-        sc[k] = *reinterpret_cast<const float*>(tok + kDimCkv + 4 * (lane >> 3));
-        if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
-      } else {
-        const uint4* tok = reinterpret_cast<const uint4*>(p.ckv_cache + (size_t)slot * kDimCkv + 16 * lane);
-        lat[k][0] = tok[0];
-        lat[k][1] = tok[1];
-        if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * lane);
-      }
+    const uint32_t bad = copy_tokens<kFp8, kTok>(p, (size_t)row + warp * kTok, mine);
+    const uint32_t keys = __ballot_sync(0xffffffffu, mine >= 0 && mine < p.num_slots);
+    if (lane == 0) {
+      if (keys) atomicOr(&is_key, keys << (warp * kTok));
+      if (bad) atomicOr(&is_odd, bad << (warp * kTok));
     }
-#pragma unroll
-    for (int k = 0; k < kTok; ++k) {
-      uint4 a, b;
-      if constexpr (kFp8) {
-        a = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(lat[k][0].x, lat[k][0].y), sc[k]);
-        b = ptx::e4m3x8_scaled_to_bf16x8(make_uint2(lat[k][0].z, lat[k][0].w), sc[k]);
-      } else {
-        a = lat[k][0];
-        b = lat[k][1];
-      }
-      const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, rope[k].x, rope[k].y, rope[k].z, rope[k].w};
-      uint32_t odd = 0;
-#pragma unroll
-      for (int i = 0; i < 12; ++i) odd |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);  // exponent all ones
-      const bool bad = __any_sync(0xffffffffu, odd != 0);
-      if (bad) a = b = rope[k] = make_uint4(0, 0, 0, 0);
-      const size_t row = (size_t)tile * kChunkKeys + k0 + k;
-      uint4* dst = reinterpret_cast<uint4*>(p.ckv + row * kDimCkv + 16 * lane);
-      dst[0] = a;
-      dst[1] = b;
-      if (lane < 8) *reinterpret_cast<uint4*>(p.kpe + row * kDimKpe + 8 * lane) = rope[k];
-      if (lane == 0 && bad) atomicOr(&is_odd, 1u << ((k0 + k) & 31));
-    }
-    const unsigned keys = __ballot_sync(0xffffffffu, mine >= 0);
-    if (lane == 0 && keys) atomicOr(&is_key, keys << (k0 & 31));
     __syncthreads();
     if (threadIdx.x == 0) {
-      p.flags[(size_t)tile * 8 + first / 32] = is_key;
-      p.flags[(size_t)tile * 8 + 4 + first / 32] = is_odd;
+      p.flags[row / 32] = is_key;
+      p.flags[(size_t)p.tiles * 4 + row / 32] = is_odd;
+      if (kSpan == kShared && row % kHalfKeys == 0) p.infos[row / kHalfKeys] = src.info;
     }
+  }
+}
+
+// The same where whole halves may be read from the cache (p.sources): a warp looks at a half's 64
+// slots; if they are all keys of all rows that read it and follow one another, it notes the
+// first.  The block's warps then copy the others together, eight rows each.
+template <int kSpan>
+__global__ void __launch_bounds__(kStageThreads) span_source_kernel(const ChunkParams p, int halves_per_block) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0) {
+    plan<kSpan>(p);
+    return;
+  }
+  constexpr int kWarps = kStageThreads / 32, kTok = kHalfKeys / kWarps;
+  __shared__ int slots[kWarps][kHalfKeys], rows[kWarps];
+  __shared__ uint32_t is_odd[kWarps][2];
+  __shared__ OwnTable own;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const StagedRows<kSpan> staged(p, &own);
+  const int halves = staged.rows / kHalfKeys;
+  for (int first = (blockIdx.x - 1) * halves_per_block; first < halves; first += (gridDim.x - 1) * halves_per_block) {
+    int copy_row = -1;
+    const int nth = first + warp;
+    if (warp < halves_per_block && nth < halves) {
+      int row;
+      RowSource src;
+      if (staged.source(p, &own, nth * kHalfKeys, &row, &src)) {
+        if (kSpan == kShared && lane == 0) p.infos[row / kHalfKeys] = src.info;
+        int s[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = src.from + 32 * h + lane;
+          s[h] = src.holds(key) ? __ldg(src.list + key) : -1;
+        }
+        const int slot = __shfl_sync(0xffffffffu, s[0], 0);
+        const bool run = src.direct && slot >= 0 && slot <= p.num_slots - kHalfKeys && s[0] == slot + lane &&
+                         s[1] == slot + 32 + lane;
+        if (__all_sync(0xffffffffu, run)) {
+          if (lane == 0) p.sources[row / kHalfKeys] = slot;
+        } else {
+          copy_row = row;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            slots[warp][32 * h + lane] = s[h];
+            const uint32_t keys = __ballot_sync(0xffffffffu, s[h] >= 0 && s[h] < p.num_slots);
+            if (lane == 0) p.flags[row / 32 + h] = keys;
+          }
+          if (lane == 0) p.sources[row / kHalfKeys] = -1;
+        }
+      }
+    }
+    if (lane == 0) {
+      rows[warp] = copy_row;
+      is_odd[warp][0] = is_odd[warp][1] = 0;
+    }
+    __syncthreads();
+    for (int i = 0; i < halves_per_block; ++i) {
+      const int row = rows[i];
+      if (row < 0) continue;
+      const int mine = slots[i][warp * kTok + (lane & (kTok - 1))];
+      uint32_t bad = copy_tokens<false, kTok / 2>(p, (size_t)row + warp * kTok, mine);
+      bad |= copy_tokens<false, kTok / 2>(p, (size_t)row + warp * kTok + kTok / 2,
+                                         __shfl_sync(0xffffffffu, mine, (lane + kTok / 2) & 31)) << (kTok / 2);
+      if (lane == 0 && bad) atomicOr(&is_odd[i][warp / 4], bad << (warp % 4 * kTok));
+    }
+    __syncthreads();
+    if (warp < halves_per_block && copy_row >= 0 && lane < 2)
+      p.flags[(size_t)p.tiles * 4 + copy_row / 32 + lane] = is_odd[warp][lane];
+    __syncthreads();  // (before the next round's rows)
   }
 }
 
@@ -399,8 +602,17 @@ cudaError_t launch_validate_groups(const ChunkParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_span_stage(const ChunkParams& p, int span, bool fp8, cudaStream_t stream) {
+  if (p.sources) {
+    // One half a block while they fit a wave, so that copies start at once; else a warp each.
+    const int halves = p.tiles * 2, each = halves <= 152 * 8 ? 1 : kStageThreads / 32;
+    const int blocks = (halves + each - 1) / each, grid = 1 + (blocks < 152 * 8 ? blocks : 152 * 8);
+    if (span == kWindow) span_source_kernel<kWindow><<<grid, kStageThreads, 0, stream>>>(p, each);
+    else span_source_kernel<kShared><<<grid, kStageThreads, 0, stream>>>(p, each);
+    return cudaGetLastError();
+  }
   const int parts = p.tiles * (kChunkKeys / kStageKeys);  // (tiles * 128 is below 2^31)
-  const int grid = 1 + (parts < 152 * 32 ? parts : 152 * 32);
+  const int most = span == kShared ? 152 * 4 : 152 * 32;  // (kShared: every block makes the table of own halves)
+  const int grid = 1 + (parts < most ? parts : most);
   if (span == kWindow) {
     if (fp8) span_stage_kernel<true, kWindow><<<grid, kStageThreads, 0, stream>>>(p);
     else span_stage_kernel<false, kWindow><<<grid, kStageThreads, 0, stream>>>(p);

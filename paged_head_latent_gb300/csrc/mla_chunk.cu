@@ -228,67 +228,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == kKWarp || warp == kVWarp) {
     // ------------------------------------------------------------ loads
-    if (lane == 0 && sound) {
+    // A lane has a box of its own (K's and Q's nine chunks, V's four for each half), so that a group
+    // of them leaves in one instruction: a product waits for its operands as long as they are
+    // reloaded, and a thread that issued them one after another cost 5 to 10 % of a tile.
+    if (sound) {
       const bool is_k = warp == kKWarp;
       const bool fault = is_k && p.fault_skip_tile >= 1 && w == 0 && rank == 0;
       bool ok = true;
+      // (the whole warp waits, and leaves together)
+      auto wait = [&](uint32_t i, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort, p.status, kStatusTimeout, p.wait_ns));
+      };
+      const int half = is_k ? (int)rank : lane >> 2 & 1;  // of the tile's keys
+      const int chunk = is_k ? lane : 4 * (int)rank + (lane & 3);
+      const uint32_t dst = base + (is_k ? kOffK : kOffV) + lane * kBox;
+      const int column = chunk < 8 ? 64 * chunk : 0;
+      const CUtensorMap* const staged = chunk < 8 ? &maps.ckv : &maps.kpe;
+      const CUtensorMap* const cached = chunk < 8 ? &maps.cache_ckv : &maps.cache_kpe;
+      const uint32_t group = is_k ? lane / kGroup : lane >> 2;  // (lanes without a box have one past the last)
+      const uint32_t full = leader((is_k ? K_FULL : V_FULL) + min(group, is_k ? kKGroups - 1 : 1)), q_full = leader(Q_FULL);
       uint32_t j = 0;
-      // The staged rows of a tile's halves; or the cache slots, which are read a tile ahead.
-      int rows[2], slots[2] = {-1, -1};
+      // Where the lane's half of the next tile is: its staged row, or the cache slot.
+      int next_row = 0, next_slot = -1;
       Walk ahead(p, w);
       auto look = [&]() {
         if (!ahead.live) return;
         if constexpr (kSpan == kCausal) {
-          rows[0] = (ahead.blk.tile0 + ahead.t) * kChunkKeys;
-          rows[1] = rows[0] + kHalfKeys;
+          next_row = (ahead.blk.tile0 + ahead.t) * kChunkKeys + kHalfKeys * half;
         } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            rows[h] = half_row<kSpan>(p, ahead, h);
-            if (kDirect) slots[h] = __ldcg(p.sources + rows[h] / kHalfKeys);
-          }
+          next_row = half_row<kSpan>(p, ahead, half);
+          if (kDirect) next_slot = __ldcg(p.sources + next_row / kHalfKeys);
         }
       };
       look();
       for (; ahead.live && ok; ++j) {
         const bool first = ahead.first();
-        const int q_row = ahead.blk.row0, row[2] = {rows[0], rows[1]}, slot[2] = {slots[0], slots[1]};
+        const int q_row = ahead.blk.row0;
+        const bool direct = kDirect && next_slot >= 0;
+        const int row = direct ? next_slot : next_row;
+        const CUtensorMap* map = direct ? cached : staged;
         ahead.advance();
         look();
-        auto load = [&](uint32_t dst, int c, uint32_t h, uint32_t to) {  // columns 64 c .. of half h's keys
-          const bool cached = kDirect && (h ? slot[1] : slot[0]) >= 0;
-          const CUtensorMap* map = c < 8 ? (cached ? &maps.cache_ckv : &maps.ckv) : (cached ? &maps.cache_kpe : &maps.kpe);
-          tma_load_pair(dst, map, c < 8 ? 64 * c : 0, cached ? (h ? slot[1] : slot[0]) : h ? row[1] : row[0], to);
-        };
         const uint32_t again = (j - 1) & 1;  // phase of the previous use of a buffer
         if (is_k) {
           if (fault && (int)j == p.fault_skip_tile) break;  // (test of the give-up path: no more loads)
 #pragma unroll
-          for (uint32_t g = 0; g < kKGroups && ok; ++g) {
-            if (j > 0)
-              ok = g < kKGroups - 1 ? mbar_wait(bar(K_EMPTY + g), again, abort, p.status, kStatusTimeout, p.wait_ns)
-                                    : mbar_wait(bar(S_FULL + again), ((j - 1) >> 1) & 1, abort, p.status, kStatusTimeout, p.wait_ns);
-            if (!ok) break;
-            if (rank == 0) mbar_arrive_expect_tx(bar(K_FULL + g), 2 * kGroup * kBox);
-#pragma unroll
-            for (int c = kGroup * g; c < (int)(kGroup * (g + 1)); ++c)
-              load(base + kOffK + c * kBox, c, rank, leader(K_FULL + g));
+          for (uint32_t g = 0; g < kKGroups; ++g) {
+            if (j > 0 && !(ok = g < kKGroups - 1 ? wait(K_EMPTY + g, again) : wait(S_FULL + again, ((j - 1) >> 1) & 1))) break;
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(K_FULL + g), 2 * kGroup * kBox);
+            if (group == g) tma_load_pair(dst, map, column, row, full);
           }
           if (first && ok) {  // (the previous block's last S is done, so Q is free)
-            if (rank == 0) mbar_arrive_expect_tx(bar(Q_FULL), 2 * kKBoxes * kBox);
-            for (int c = 0; c < kKBoxes; ++c)
-              tma_load_pair(base + kOffQ + c * kBox, c < 8 ? &maps.q_nope : &maps.q_pe, c < 8 ? 64 * c : 0,
-                            q_row + 64 * rank, leader(Q_FULL));
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(Q_FULL), 2 * kKBoxes * kBox);
+            if (lane < kKBoxes)
+              tma_load_pair(base + kOffQ + lane * kBox, lane < 8 ? &maps.q_nope : &maps.q_pe, column, q_row + 64 * rank, q_full);
           }
         } else {
 #pragma unroll
-          for (uint32_t h = 0; h < 2 && ok; ++h) {  // keys 64 h .. + 63, this SM's 256 columns
-            if (j > 0) ok = mbar_wait(bar(h ? PV_DONE : V_EMPTY), again, abort, p.status, kStatusTimeout, p.wait_ns);
-            if (!ok) break;
-            if (rank == 0) mbar_arrive_expect_tx(bar(V_FULL + h), 8 * kBox);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              load(base + kOffV + (4 * h + c) * kBox, 4 * (int)rank + c, h, leader(V_FULL + h));
+          for (uint32_t h = 0; h < 2; ++h) {  // keys 64 h .. + 63, this SM's 256 columns
+            if (j > 0 && !(ok = wait(h ? PV_DONE : V_EMPTY, again))) break;
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(V_FULL + h), 8 * kBox);
+            if (group == h) tma_load_pair(dst, map, column, row, full);
           }
         }
       }
@@ -370,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* red = reinterpret_cast<float*>(smem + kOffRed);
     const int quarter = 2 * half + part;
     const uint32_t mine = base + kOffP + half * kBox + r * 128;  // this thread's row of P
-    const uint32_t piece = base + kOffP + half * kBox + (warp & 1) * 4096 + part * 2048;  // 2 KB of P for the output
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     const uint32_t col_s = tmem + lanes + kColS + 32 * part, col_o = tmem + lanes + kColO + 128 * part;
     const uint32_t p_full = leader(P_FULL), o_empty = leader(O_EMPTY);
     const float scale = p.scale_log2;
@@ -580,61 +580,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else
             p.part_lse[frag + in_block + lane] = total == 0.f ? -INFINITY : m_ref + log2f(total);
         }
-        uint32_t o[2][32];
-        tmem_ld32(col_o, o[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 32 columns at a time, the next ones under way
-          uint32_t(&x)[32] = o[c & 1];
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {  // (rolled: its code must not push the tiles' code out of the instruction cache)
+          uint32_t x[32];
+          tmem_ld32(col_o + 32 * c, x);
           tmem_ld_wait();
-          if (c < 3) {
-            tmem_ld32(col_o + 32 * (c + 1), o[(c + 1) & 1]);
-          } else {  // O is in registers: the next block's products may begin
+          if (c == 3) {  // O is in registers: the next block's products may begin
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader(o_empty);
           }
+          if (in_block + lane >= it.blk.rows) continue;
+          float y[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(x[k]) * inv;
           if (whole) {
-            // Through this warp's part of P, so that a store writes 64 contiguous bytes of 8 rows.
+            uint32_t h[16];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float a = __uint_as_float(x[8 * u + 2 * e]), b = __uint_as_float(x[8 * u + 2 * e + 1]);
-                const __nv_bfloat162 h = __floats2bfloat162_rn(a * inv, b * inv);
-                y[e] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)),
-                           "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                           : "memory");
+            for (int k = 0; k < 16; ++k) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
+              h[k] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            __syncwarp();
+            __nv_bfloat16* dst = p.out + ((size_t)it.blk.row0 + in_block + lane) * kDimCkv + 256 * half + 128 * part + 32 * c;
+            if (wide) {
+              st_global_v8(dst, h);
+              st_global_v8(dst + 16, h + 8);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = 8 * i + (lane >> 2), u = lane & 3;
-              uint4 v;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                           : "r"(piece + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4))
-                           : "memory");
-              if (in_block + rr < it.blk.rows)
-                *reinterpret_cast<uint4*>(p.out + ((size_t)it.blk.row0 + in_block + rr) * kDimCkv + 256 * half + 128 * part +
-                                          32 * c + 8 * u) = v;
+              for (int u = 0; u < 4; ++u)
+                reinterpret_cast<uint4*>(dst)[u] = make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
             }
-            __syncwarp();
           } else {
             // A fragment lies as [column / 4][row][4], so a store is 512 contiguous bytes.
             float4* dst = reinterpret_cast<float4*>(p.part_o + frag * kDimCkv) + (64 * half + 32 * part + 8 * c) * kChunkRows +
                           in_block + lane;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              float4 y;
-              y.x = __uint_as_float(x[4 * u]) * inv;
-              y.y = __uint_as_float(x[4 * u + 1]) * inv;
-              y.z = __uint_as_float(x[4 * u + 2]) * inv;
-              y.w = __uint_as_float(x[4 * u + 3]) * inv;
-              dst[u * kChunkRows] = y;
-            }
+            for (int u = 0; u < 8; ++u) dst[u * kChunkRows] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
           }
         }
         l = 0.f;

@@ -103,6 +103,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same in less code (a quarter of it where it is inlined), for a kernel whose loops have to share
+// the instruction cache.  Times are in units of 1024 ns.
+__device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status,
+                                                uint32_t timeout_bit, uint32_t limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = static_cast<uint32_t>(globaltimer() >> 10);
+#pragma unroll 1
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (!*abort && static_cast<uint32_t>(globaltimer() >> 10) - t0 <= limit);
+  if (!*abort) atomicOr(status, timeout_bit);
+  *abort = 1;
+  return false;
+}
+
 // ---------------------------------------------------------------- fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -145,6 +160,13 @@ __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap
 __device__ __forceinline__ void st_global_v4_hint(void* ptr, uint4 v, uint64_t pol) {
   asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(ptr), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w), "l"(pol)
+               : "memory");
+}
+
+// 32-byte global store (32-byte aligned).
+__device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 

@@ -14,24 +14,58 @@ from typing import Tuple
 
 import torch
 
-from . import HEAD_DIM_CKV, HEAD_DIM_KPE, MlaDims, lib, make_dims
-from .cache import _BF16, _F32, _I32, _U8, _at, _bf16_caches, _buffer, _call, _check, _fp8_cache, _scratch
+from . import HEAD_DIM_CKV, HEAD_DIM_KPE, MlaDims, _cache_geometry, lib
+from .cache import _BF16, _F32, _I32, _U8, _buffer, _call, _check, _fp8_cache, _scratch
 
 
 # ---------------------------------------------------------------- the calls' common part
-def _attend(name, q_nope, q_pe, cache, geometry, qo_indptr, kv_indptr, kv_indices, middle, size, sm_scale, out, lse,
+def _good(index, dtype, *tensors):
+    """Whether these are contiguous tensors of ``dtype`` on CUDA device ``index``: the conditions that
+    hold for good arguments, tested together (one check after the other took as long as the GPU's
+    part of a small call)."""
+    try:
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return index >= 0
+
+
+def _at(t):
+    """The address of a tensor (what is none is refused by its check)."""
+    return t.data_ptr() if isinstance(t, torch.Tensor) else None
+
+
+def _numel(t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("the lists must be torch.Tensors")
+    return t.numel()
+
+
+def _attend(name, q_nope, q_pe, cache, qo_indptr, ints, kv_indptr, kv_indices, middle, size, sm_scale, out, lse,
             workspace, flags, num_workers, stream):
-    """``middle(index)``: the arguments between the caches (and qo_indptr) and sm_scale, checked;
-    ``size(dims)``: the workspace that the call needs."""
+    """``ints``: the names and tensors of the call's own lists; ``middle``: the arguments between the
+    caches (and qo_indptr) and sm_scale; ``size``: (function, arguments) of the workspace size."""
+    _check("q_nope", q_nope, _BF16)
     index = q_nope.get_device()
-    _check("q_pe", q_pe, _BF16, index)
-    if q_nope.dim() != 3:
-        raise ValueError("q_nope must be [rows, H, 512]")
-    rows, heads = q_nope.shape[0], q_nope.shape[1]
-    if q_nope.shape != (rows, heads, HEAD_DIM_CKV) or q_pe.shape != (rows, heads, HEAD_DIM_KPE):
+    shape = q_nope.shape
+    fp8 = len(cache) == 1
+    if not (_good(index, _BF16, q_pe, *(() if fp8 else cache)) and _good(index, _I32, kv_indptr, kv_indices, *ints.values())
+            and (not fp8 or _good(index, _U8, *cache)) and (qo_indptr is None or _good(index, _I32, qo_indptr))):
+        _check("q_pe", q_pe, _BF16, index)
+        for n, t in zip(("kv_fp8",) if fp8 else ("ckv_cache", "kpe_cache"), cache):
+            _check(n, t, _U8 if fp8 else _BF16, index)
+        for n, t in (("kv_indptr", kv_indptr), ("kv_indices", kv_indices), *ints.items()):
+            _check(n, t, _I32, index)
+        _check("qo_indptr", qo_indptr, _I32, index)
+    if fp8:
+        num_pages, page_size = _fp8_cache(cache[0], index)
+    else:
+        num_pages, page_size = _cache_geometry(*cache)
+    if len(shape) != 3 or shape[2] != HEAD_DIM_CKV or q_pe.shape != (shape[0], shape[1], HEAD_DIM_KPE):
         raise ValueError("q_nope must be [rows, H, 512] and q_pe [rows, H, 64]")
-    _check("kv_indptr", kv_indptr, _I32, index)
-    _check("kv_indices", kv_indices, _I32, index)
+    rows, heads, _ = shape
     batch = kv_indptr.numel() - 1
     if batch < 0:
         raise ValueError("kv_indptr must have batch + 1 entries")
@@ -40,35 +74,21 @@ def _attend(name, q_nope, q_pe, cache, geometry, qo_indptr, kv_indptr, kv_indice
             raise ValueError("decode: q_nope.shape[0] must equal len(kv_indptr) - 1")
         first = ()
     else:
-        _check("qo_indptr", qo_indptr, _I32, index)
         if qo_indptr.numel() != batch + 1:
             raise ValueError("qo_indptr and kv_indptr must both have batch + 1 entries")
         first = (qo_indptr.data_ptr(),)
-    middle = middle(index)
-    dims = make_dims(batch, heads, geometry[0], geometry[1], kv_indices.numel(), total_q=rows, num_workers=num_workers)
-    out = _buffer("out", out, (rows, heads, HEAD_DIM_CKV), _BF16, q_nope, stream)
+    dims = MlaDims(batch, heads, HEAD_DIM_CKV, HEAD_DIM_KPE, num_pages, page_size, rows, kv_indices.numel(), num_workers)
+    out = _buffer("out", out, shape, _BF16, q_nope, stream)
     lse = _buffer("lse", lse, (rows, heads), _F32, q_nope, stream)
     if workspace is None:
         with torch.cuda.device(index):
-            need = size(dims)
+            need = size[0](dims, *size[1:])
         workspace = _scratch(torch.zeros, need, q_nope, stream, name + ": workspace size")
-    else:  # (the library checks its size)
+    elif not _good(index, _U8, workspace):  # (the library checks its size)
         _check("workspace", workspace, _U8, index)
-    _call(name, index, stream, q_nope.data_ptr(), q_pe.data_ptr(), *cache, *first, *middle, float(sm_scale),
-          out.data_ptr(), lse.data_ptr(), ctypes.byref(dims), workspace.data_ptr(), workspace.numel(), int(flags))
+    _call(name, index, stream, q_nope.data_ptr(), q_pe.data_ptr(), *[t.data_ptr() for t in cache], *first, *middle,
+          sm_scale, out.data_ptr(), lse.data_ptr(), ctypes.byref(dims), workspace.data_ptr(), workspace.numel(), flags)
     return out, lse
-
-
-def _bf16(q_nope, ckv_cache, kpe_cache):
-    _check("q_nope", q_nope, _BF16)
-    geometry = _bf16_caches(ckv_cache, kpe_cache, q_nope.get_device())
-    return (ckv_cache.data_ptr(), kpe_cache.data_ptr()), geometry
-
-
-def _fp8(q_nope, kv_fp8):
-    _check("q_nope", q_nope, _BF16)
-    geometry = _fp8_cache(kv_fp8, q_nope.get_device())
-    return (kv_fp8.data_ptr(),), geometry
 
 
 # ---------------------------------------------------------------- sliding windows with sinks
@@ -83,10 +103,10 @@ def _window(name, q_nope, q_pe, cache, qo_indptr, kv_indptr, kv_indices, window,
     window, sinks = int(window), int(sinks)
     if not 1 <= window < 2 ** 31 or not 0 <= sinks < 2 ** 31:
         raise ValueError("window must be at least 1 and sinks at least 0, both int32")
-    return _attend(name, q_nope, q_pe, *cache, qo_indptr, kv_indptr, kv_indices,
-                   lambda index: (kv_indptr.data_ptr(), kv_indices.data_ptr(), window, sinks),
-                   lambda dims: workspace_bytes_window(dims, window, sinks, qo_indptr is not None), sm_scale, out, lse,
-                   workspace, flags, num_workers, stream)
+    return _attend(name, q_nope, q_pe, cache, qo_indptr, {}, kv_indptr, kv_indices,
+                   (_at(kv_indptr), _at(kv_indices), window, sinks),
+                   (workspace_bytes_window, window, sinks, qo_indptr is not None), sm_scale, out, lse, workspace, flags,
+                   num_workers, stream)
 
 
 def mla_paged_decode_window(q_nope, q_pe, ckv_cache, kpe_cache, kv_indptr, kv_indices, window, sinks, sm_scale,
@@ -94,7 +114,7 @@ def mla_paged_decode_window(q_nope, q_pe, ckv_cache, kpe_cache, kv_indptr, kv_in
                             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """One query token per request over the last ``window`` and the first ``sinks`` of its keys.
     Arguments as for ``mla_paged_decode``; the lists name all keys of a request.  Returns (out, lse)."""
-    return _window("mla_paged_decode_window", q_nope, q_pe, _bf16(q_nope, ckv_cache, kpe_cache), None, kv_indptr,
+    return _window("mla_paged_decode_window", q_nope, q_pe, (ckv_cache, kpe_cache), None, kv_indptr,
                    kv_indices, window, sinks, sm_scale, out, lse, workspace, flags, num_workers, stream)
 
 
@@ -102,7 +122,7 @@ def mla_paged_decode_window_fp8(q_nope, q_pe, kv_fp8, kv_indptr, kv_indices, win
                                 workspace=None, flags=0, num_workers=0,
                                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """``mla_paged_decode_window`` over an FP8 cache kv_fp8 [num_pages, page_size, 656]."""
-    return _window("mla_paged_decode_window_fp8", q_nope, q_pe, _fp8(q_nope, kv_fp8), None, kv_indptr, kv_indices,
+    return _window("mla_paged_decode_window_fp8", q_nope, q_pe, (kv_fp8,), None, kv_indptr, kv_indices,
                    window, sinks, sm_scale, out, lse, workspace, flags, num_workers, stream)
 
 
@@ -111,7 +131,7 @@ def mla_paged_prefill_window(q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, kv_i
                              stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Causal attention of a chunk of new tokens in which every token sees the last ``window``
     keys up to its own and the first ``sinks``.  Arguments as for ``mla_paged_prefill_staged``."""
-    return _window("mla_paged_prefill_window", q_nope, q_pe, _bf16(q_nope, ckv_cache, kpe_cache), qo_indptr, kv_indptr,
+    return _window("mla_paged_prefill_window", q_nope, q_pe, (ckv_cache, kpe_cache), qo_indptr, kv_indptr,
                    kv_indices, window, sinks, sm_scale, out, lse, workspace, flags, num_workers, stream)
 
 
@@ -119,7 +139,7 @@ def mla_paged_prefill_window_fp8(q_nope, q_pe, kv_fp8, qo_indptr, kv_indptr, kv_
                                  out=None, lse=None, workspace=None, flags=0, num_workers=0,
                                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """``mla_paged_prefill_window`` over an FP8 cache kv_fp8 [num_pages, page_size, 656]."""
-    return _window("mla_paged_prefill_window_fp8", q_nope, q_pe, _fp8(q_nope, kv_fp8), qo_indptr, kv_indptr, kv_indices,
+    return _window("mla_paged_prefill_window_fp8", q_nope, q_pe, (kv_fp8,), qo_indptr, kv_indptr, kv_indices,
                    window, sinks, sm_scale, out, lse, workspace, flags, num_workers, stream)
 
 
@@ -133,19 +153,15 @@ def workspace_bytes_shared(dims: MlaDims, groups: int, num_prefix_indices: int, 
 
 def _shared(name, q_nope, q_pe, cache, qo_indptr, group_indptr, prefix_indptr, prefix_indices, kv_indptr, kv_indices,
             sm_scale, out, lse, workspace, flags, num_workers, stream):
-    def middle(index):
-        _check("group_indptr", group_indptr, _I32, index)
-        _check("prefix_indptr", prefix_indptr, _I32, index)
-        _check("prefix_indices", prefix_indices, _I32, index)
-        if group_indptr.numel() < 1 or prefix_indptr.numel() != group_indptr.numel():
-            raise ValueError("group_indptr and prefix_indptr must both have groups + 1 entries")
-        return (group_indptr.data_ptr(), group_indptr.numel() - 1, prefix_indptr.data_ptr(), prefix_indices.data_ptr(),
-                prefix_indices.numel(), kv_indptr.data_ptr(), kv_indices.data_ptr())
-
-    return _attend(name, q_nope, q_pe, *cache, qo_indptr, kv_indptr, kv_indices, middle,
-                   lambda dims: workspace_bytes_shared(dims, group_indptr.numel() - 1, prefix_indices.numel(),
-                                                       qo_indptr is not None), sm_scale, out, lse, workspace, flags,
-                   num_workers, stream)
+    groups, num_prefix = _numel(group_indptr) - 1, _numel(prefix_indices)
+    if groups < 0 or _numel(prefix_indptr) != groups + 1:
+        raise ValueError("group_indptr and prefix_indptr must both have groups + 1 entries")
+    return _attend(name, q_nope, q_pe, cache, qo_indptr,
+                   {"group_indptr": group_indptr, "prefix_indptr": prefix_indptr, "prefix_indices": prefix_indices},
+                   kv_indptr, kv_indices, (group_indptr.data_ptr(), groups, prefix_indptr.data_ptr(),
+                                           prefix_indices.data_ptr(), num_prefix, _at(kv_indptr), _at(kv_indices)),
+                   (workspace_bytes_shared, groups, num_prefix, qo_indptr is not None), sm_scale, out, lse, workspace,
+                   flags, num_workers, stream)
 
 
 def mla_paged_decode_shared(q_nope, q_pe, ckv_cache, kpe_cache, group_indptr, prefix_indptr, prefix_indices, kv_indptr,
@@ -154,7 +170,7 @@ def mla_paged_decode_shared(q_nope, q_pe, ckv_cache, kpe_cache, group_indptr, pr
     """One query token per request over the keys that its group shares (``prefix_*``) and those of
     its own (``kv_*``).  Group g: requests group_indptr[g] .. group_indptr[g + 1] - 1;
     ``block_table_to_shared_csr`` makes all five lists.  Returns (out, lse)."""
-    return _shared("mla_paged_decode_shared", q_nope, q_pe, _bf16(q_nope, ckv_cache, kpe_cache), None, group_indptr,
+    return _shared("mla_paged_decode_shared", q_nope, q_pe, (ckv_cache, kpe_cache), None, group_indptr,
                    prefix_indptr, prefix_indices, kv_indptr, kv_indices, sm_scale, out, lse, workspace, flags,
                    num_workers, stream)
 
@@ -163,7 +179,7 @@ def mla_paged_decode_shared_fp8(q_nope, q_pe, kv_fp8, group_indptr, prefix_indpt
                                 kv_indices, sm_scale, out=None, lse=None, workspace=None, flags=0, num_workers=0,
                                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """``mla_paged_decode_shared`` over an FP8 cache kv_fp8 [num_pages, page_size, 656]."""
-    return _shared("mla_paged_decode_shared_fp8", q_nope, q_pe, _fp8(q_nope, kv_fp8), None, group_indptr, prefix_indptr,
+    return _shared("mla_paged_decode_shared_fp8", q_nope, q_pe, (kv_fp8,), None, group_indptr, prefix_indptr,
                    prefix_indices, kv_indptr, kv_indices, sm_scale, out, lse, workspace, flags, num_workers, stream)
 
 
@@ -172,7 +188,7 @@ def mla_paged_prefill_shared(q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, grou
                              num_workers=0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Ragged chunks of new tokens behind a shared prefix: every token sees the whole prefix of
     its group, and causally the keys of its own request (``kv_*``: the new tokens' among them)."""
-    return _shared("mla_paged_prefill_shared", q_nope, q_pe, _bf16(q_nope, ckv_cache, kpe_cache), qo_indptr,
+    return _shared("mla_paged_prefill_shared", q_nope, q_pe, (ckv_cache, kpe_cache), qo_indptr,
                    group_indptr, prefix_indptr, prefix_indices, kv_indptr, kv_indices, sm_scale, out, lse, workspace,
                    flags, num_workers, stream)
 
@@ -181,7 +197,7 @@ def mla_paged_prefill_shared_fp8(q_nope, q_pe, kv_fp8, qo_indptr, group_indptr, 
                                  kv_indptr, kv_indices, sm_scale, out=None, lse=None, workspace=None, flags=0,
                                  num_workers=0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """``mla_paged_prefill_shared`` over an FP8 cache kv_fp8 [num_pages, page_size, 656]."""
-    return _shared("mla_paged_prefill_shared_fp8", q_nope, q_pe, _fp8(q_nope, kv_fp8), qo_indptr, group_indptr,
+    return _shared("mla_paged_prefill_shared_fp8", q_nope, q_pe, (kv_fp8,), qo_indptr, group_indptr,
                    prefix_indptr, prefix_indices, kv_indptr, kv_indices, sm_scale, out, lse, workspace, flags,
                    num_workers, stream)
 
@@ -221,10 +237,10 @@ def block_table_to_shared_csr(block_table, seq_lens, page_size, min_shared=1, pr
     capacity = _room("kv_indices", capacity, kv_indices, batch * most)
     group_indptr = _buffer("group_indptr", group_indptr, (batch + 1,), _I32, block_table, stream)
     prefix_indptr = _buffer("prefix_indptr", prefix_indptr, (batch + 1,), _I32, block_table, stream)
-    prefix_indices = _buffer("prefix_indices", prefix_indices, (prefix_capacity,), _I32, block_table, stream)
     kv_indptr = _buffer("kv_indptr", kv_indptr, (batch + 1,), _I32, block_table, stream)
+    prefix_indices = _buffer("prefix_indices", prefix_indices, (prefix_capacity,), _I32, block_table, stream)
     kv_indices = _buffer("kv_indices", kv_indices, (capacity,), _I32, block_table, stream)
     _call("mla_block_table_to_shared_csr", index, stream, block_table.data_ptr(), seq_lens.data_ptr(), batch, max_blocks,
-          page_size, min_shared, group_indptr.data_ptr(), prefix_indptr.data_ptr(), _at(prefix_indices), prefix_capacity,
-          kv_indptr.data_ptr(), _at(kv_indices), capacity)
+          page_size, min_shared, group_indptr.data_ptr(), prefix_indptr.data_ptr(), prefix_indices.data_ptr(), prefix_capacity,
+          kv_indptr.data_ptr(), kv_indices.data_ptr(), capacity)
     return group_indptr, prefix_indptr, prefix_indices, kv_indptr, kv_indices

@@ -13,7 +13,8 @@ namespace mla {
 namespace {
 
 constexpr int kStageThreads = 256;
-constexpr int kStageKeys = 32;  // keys of a staging block: one word of the tile's flags
+constexpr int kStageRows = 8;   // staged rows that a warp takes at a time: one byte of the flags
+constexpr int kStageBlocks = 152 * 3, kSourceBlocks = 152 * 4;  // blocks of threads that run at a time
 constexpr int kNear = 1024;     // entries of the plan's tables that are kept in shared memory too
 constexpr int kBlockCost = 3;   // cost units (tiles) of starting a block, as in the staged prefill
 
@@ -409,100 +410,119 @@ struct StagedRows {
   }
 };
 
-// Eight threads' worth of tokens at a time: the staged rows `row` .. + kTok - 1 of this warp, from
-// the cache's slots `mine` (lanes 0 .. kTok - 1; outside the cache: zeros).  Returns, to all lanes, the
-// rows that hold a value that is not finite (their values are written as zeros, so that a
-// weight of zero always makes a zero product).
+// kTok tokens of a warp on their way from the cache.  A lane has latent values 8 lane .. + 7 and
+// 256 + 8 lane .. + 7, and rope values 8 lane .. + 7.
 template <bool kFp8, int kTok>
-__device__ __forceinline__ uint32_t copy_tokens(const ChunkParams& p, size_t row, int mine) {
-  const int lane = threadIdx.x & 31;
-  // A lane has latent values 8 lane .. + 7 and 256 + 8 lane .. + 7, rope values 8 lane .. + 7.
-  uint4 lat[kTok][2], rope[kTok];
-  uint2 code[kTok][2];
-  float sc[kTok][2];
-#pragma unroll
-  for (int k = 0; k < kTok; ++k) {
-    const int slot = __shfl_sync(0xffffffffu, mine, k);
-    lat[k][0] = lat[k][1] = rope[k] = make_uint4(0, 0, 0, 0);
-    code[k][0] = code[k][1] = make_uint2(0, 0);
-    sc[k][0] = sc[k][1] = 0.f;
-    if (slot < 0 || slot >= p.num_slots) continue;
-    if constexpr (kFp8) {
-      const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        code[k][h] = *reinterpret_cast<const uint2*>(tok + 256 * h + 8 * lane);
-        sc[k][h] = *reinterpret_cast<const float*>(tok + kDimCkv + 8 * h + 4 * (lane >> 4));
-      }
-      if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
-    } else {
-      const uint4* tok = reinterpret_cast<const uint4*>(p.ckv_cache + (size_t)slot * kDimCkv);
-      lat[k][0] = tok[lane];
-      lat[k][1] = tok[32 + lane];
-      if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * lane);
-    }
-  }
-  uint32_t bad = 0;
-#pragma unroll
-  for (int k = 0; k < kTok; ++k) {
-    uint4 a = lat[k][0], b = lat[k][1];
-    if constexpr (kFp8) {
-      a = ptx::e4m3x8_scaled_to_bf16x8(code[k][0], sc[k][0]);
-      b = ptx::e4m3x8_scaled_to_bf16x8(code[k][1], sc[k][1]);
-    }
-    const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, rope[k].x, rope[k].y, rope[k].z, rope[k].w};
-    uint32_t odd = 0;
-#pragma unroll
-    for (int i = 0; i < 12; ++i) odd |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);  // exponent all ones
-    if (__any_sync(0xffffffffu, odd != 0)) {
-      a = b = rope[k] = make_uint4(0, 0, 0, 0);
-      bad |= 1u << k;
-    }
-    uint4* dst = reinterpret_cast<uint4*>(p.ckv + (row + k) * kDimCkv);
-    dst[lane] = a;
-    dst[32 + lane] = b;
-    if (lane < 8) *reinterpret_cast<uint4*>(p.kpe + (row + k) * kDimKpe + 8 * lane) = rope[k];
-  }
-  return bad;
-}
+struct Tokens {
+  uint4 lat[kFp8 ? 1 : kTok][2], rope[kTok];
+  uint2 code[kFp8 ? kTok : 1][2];
+  float scale[kFp8 ? kTok : 1][2];
 
-// Block 0 makes the plan.  The others take 32 staged rows at a time, of one list, read through
+  // Ask for the tokens in slots `mine` of lanes first .. first + kTok - 1 (outside the cache: zeros).
+  __device__ __forceinline__ void ask(const ChunkParams& p, int mine, int first) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < kTok; ++k) {
+      const int slot = __shfl_sync(0xffffffffu, mine, first + k);
+      rope[k] = make_uint4(0, 0, 0, 0);
+      if constexpr (kFp8) code[k][0] = code[k][1] = make_uint2(0, 0), scale[k][0] = scale[k][1] = 0.f;
+      else lat[k][0] = lat[k][1] = make_uint4(0, 0, 0, 0);
+      if (slot < 0 || slot >= p.num_slots) continue;
+      if constexpr (kFp8) {
+        const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          code[k][h] = *reinterpret_cast<const uint2*>(tok + 256 * h + 8 * lane);
+          scale[k][h] = *reinterpret_cast<const float*>(tok + kDimCkv + 8 * h + 4 * (lane >> 4));
+        }
+        if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
+      } else {
+        const uint4* tok = reinterpret_cast<const uint4*>(p.ckv_cache + (size_t)slot * kDimCkv);
+        lat[k][0] = tok[lane];
+        lat[k][1] = tok[32 + lane];
+        if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * lane);
+      }
+    }
+  }
+  // Write them to staged rows `row` .. + kTok - 1.  Returns, to all lanes, which of them hold a value that
+  // is not finite (their values are written as zeros, so that a weight of zero always makes a
+  // zero product).
+  __device__ __forceinline__ uint32_t write(const ChunkParams& p, size_t row) {
+    const int lane = threadIdx.x & 31;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int k = 0; k < kTok; ++k) {
+      uint4 a, b;
+      if constexpr (kFp8) {
+        a = ptx::e4m3x8_scaled_to_bf16x8(code[k][0], scale[k][0]);
+        b = ptx::e4m3x8_scaled_to_bf16x8(code[k][1], scale[k][1]);
+      } else {
+        a = lat[k][0];
+        b = lat[k][1];
+      }
+      const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, rope[k].x, rope[k].y, rope[k].z, rope[k].w};
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < 12; ++i) odd |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);  // exponent all ones
+      if (__any_sync(0xffffffffu, odd != 0)) {
+        a = b = rope[k] = make_uint4(0, 0, 0, 0);
+        bad |= 1u << k;
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.ckv + (row + k) * kDimCkv);
+      dst[lane] = a;
+      dst[32 + lane] = b;
+      if (lane < 8) *reinterpret_cast<uint4*>(p.kpe + (row + k) * kDimKpe + 8 * lane) = rope[k];
+    }
+    return bad;
+  }
+};
+
+// Block 0 makes the plan.  The others' warps take 8 staged rows at a time, of one list, read through
 // their slots as the bf16 numbers that the cache holds or (kFp8) stands for.  Entries that are no
 // keys and slots outside the cache are written as zeros; the flags tell which rows are keys and
 // which of them were not finite.
+//
+// What bounds it: round trips.  A warp has four tokens on their way, and asks for its next rows'
+// slots meanwhile; with 32 rows to a block of threads, all of whose warps waited for one another,
+// 89K FP8 keys took 34 us.
 template <bool kFp8, int kSpan>
-__global__ void __launch_bounds__(kStageThreads) span_stage_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kStageThreads, 3) span_stage_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) {
     plan<kSpan>(p);
     return;
   }
-  __shared__ uint32_t is_key, is_odd;
   __shared__ OwnTable own;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kTok = kStageKeys * 32 / kStageThreads;
+  const int lane = threadIdx.x & 31, warps = (gridDim.x - 1) * (kStageThreads / 32);
   const StagedRows<kSpan> staged(p, &own);
-  for (int part = blockIdx.x - 1; part < staged.rows / kStageKeys; part += gridDim.x - 1) {
-    int row;
+  const int units = staged.rows / kStageRows;
+  int row, next_row, mine, next_mine = -1;
+  bool used, next_used;
+  auto look = [&](int unit) {  // the unit's rows, and its slots in the first lanes
     RowSource src;
-    if (!staged.source(p, &own, part * kStageKeys, &row, &src)) continue;
-    int mine = -1;
-    const int key = src.from + warp * kTok + lane;
-    if (lane < kTok && src.holds(key)) mine = __ldg(src.list + key);
-    __syncthreads();  // (the flags of the last round are written)
-    if (threadIdx.x == 0) is_key = is_odd = 0;
-    __syncthreads();
-    const uint32_t bad = copy_tokens<kFp8, kTok>(p, (size_t)row + warp * kTok, mine);
-    const uint32_t keys = __ballot_sync(0xffffffffu, mine >= 0 && mine < p.num_slots);
-    if (lane == 0) {
-      if (keys) atomicOr(&is_key, keys << (warp * kTok));
-      if (bad) atomicOr(&is_odd, bad << (warp * kTok));
+    next_used = staged.source(p, &own, unit * kStageRows, &next_row, &src);
+    next_mine = -1;
+    if (next_used) {
+      const int key = src.from + lane;
+      if (lane < kStageRows && src.holds(key)) next_mine = __ldg(src.list + key);
+      if (kSpan == kShared && next_row % kHalfKeys == 0 && lane == 0) p.infos[next_row / kHalfKeys] = src.info;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      p.flags[row / 32] = is_key;
-      p.flags[(size_t)p.tiles * 4 + row / 32] = is_odd;
-      if (kSpan == kShared && row % kHalfKeys == 0) p.infos[row / kHalfKeys] = src.info;
+  };
+  int unit = (blockIdx.x - 1) * (kStageThreads / 32) + (threadIdx.x >> 5);
+  if (unit < units) look(unit);
+  for (; unit < units; unit += warps) {
+    row = next_row, mine = next_mine, used = next_used;
+    Tokens<kFp8, kStageRows / 2> x;
+    if (used) x.ask(p, mine, 0);
+    if (unit + warps < units) look(unit + warps);
+    if (!used) continue;
+    uint32_t bad = x.write(p, row);
+    x.ask(p, mine, kStageRows / 2);
+    bad |= x.write(p, (size_t)row + kStageRows / 2) << (kStageRows / 2);
+    const uint32_t keys = __ballot_sync(0xffffffffu, mine >= 0 && mine < p.num_slots);
+    if (lane == 0) {  // (a byte has the flags of 8 rows)
+      reinterpret_cast<uint8_t*>(p.flags)[row / kStageRows] = (uint8_t)keys;
+      reinterpret_cast<uint8_t*>(p.flags + (size_t)p.tiles * 4)[row / kStageRows] = (uint8_t)bad;
     }
   }
 }
@@ -511,7 +531,7 @@ __global__ void __launch_bounds__(kStageThreads) span_stage_kernel(const ChunkPa
 // slots; if they are all keys of all rows that read it and follow one another, it notes the
 // first.  The block's warps then copy the others together, eight rows each.
 template <int kSpan>
-__global__ void __launch_bounds__(kStageThreads) span_source_kernel(const ChunkParams p, int halves_per_block) {
+__global__ void __launch_bounds__(kStageThreads, 4) span_source_kernel(const ChunkParams p, int halves_per_block) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) {
     plan<kSpan>(p);
@@ -564,9 +584,11 @@ __global__ void __launch_bounds__(kStageThreads) span_source_kernel(const ChunkP
       const int row = rows[i];
       if (row < 0) continue;
       const int mine = slots[i][warp * kTok + (lane & (kTok - 1))];
-      uint32_t bad = copy_tokens<false, kTok / 2>(p, (size_t)row + warp * kTok, mine);
-      bad |= copy_tokens<false, kTok / 2>(p, (size_t)row + warp * kTok + kTok / 2,
-                                         __shfl_sync(0xffffffffu, mine, (lane + kTok / 2) & 31)) << (kTok / 2);
+      Tokens<false, kTok / 2> x;
+      x.ask(p, mine, 0);
+      uint32_t bad = x.write(p, (size_t)row + warp * kTok);
+      x.ask(p, mine, kTok / 2);
+      bad |= x.write(p, (size_t)row + warp * kTok + kTok / 2) << (kTok / 2);
       if (lane == 0 && bad) atomicOr(&is_odd[i][warp / 4], bad << (warp % 4 * kTok));
     }
     __syncthreads();
@@ -604,15 +626,14 @@ cudaError_t launch_validate_groups(const ChunkParams& p, cudaStream_t stream) {
 cudaError_t launch_span_stage(const ChunkParams& p, int span, bool fp8, cudaStream_t stream) {
   if (p.sources) {
     // One half a block while they fit a wave, so that copies start at once; else a warp each.
-    const int halves = p.tiles * 2, each = halves <= 152 * 8 ? 1 : kStageThreads / 32;
-    const int blocks = (halves + each - 1) / each, grid = 1 + (blocks < 152 * 8 ? blocks : 152 * 8);
+    const int halves = p.tiles * 2, each = halves <= kSourceBlocks ? 1 : kStageThreads / 32;
+    const int blocks = (halves + each - 1) / each, grid = 1 + (blocks < kSourceBlocks ? blocks : kSourceBlocks);
     if (span == kWindow) span_source_kernel<kWindow><<<grid, kStageThreads, 0, stream>>>(p, each);
     else span_source_kernel<kShared><<<grid, kStageThreads, 0, stream>>>(p, each);
     return cudaGetLastError();
   }
-  const int parts = p.tiles * (kChunkKeys / kStageKeys);  // (tiles * 128 is below 2^31)
-  const int most = span == kShared ? 152 * 4 : 152 * 32;  // (kShared: every block makes the table of own halves)
-  const int grid = 1 + (parts < most ? parts : most);
+  const int blocks = (p.tiles * (kChunkKeys / kStageRows) + kStageThreads / 32 - 1) / (kStageThreads / 32);
+  const int grid = 1 + (blocks < kStageBlocks ? blocks : kStageBlocks);
   if (span == kWindow) {
     if (fp8) span_stage_kernel<true, kWindow><<<grid, kStageThreads, 0, stream>>>(p);
     else span_stage_kernel<false, kWindow><<<grid, kStageThreads, 0, stream>>>(p);

@@ -14,9 +14,11 @@ namespace {
 
 constexpr int kStageThreads = 256;
 constexpr int kStageRows = 8;   // staged rows that a warp takes at a time: one byte of the flags
-constexpr int kStageBlocks = 152 * 3, kSourceBlocks = 152 * 4;  // blocks of threads that run at a time
-constexpr int kNear = 1024;     // entries of the plan's tables that are kept in shared memory too
+constexpr int kStageBlocks = 152 * 2, kFp8Blocks = 152 * 3, kSourceBlocks = 152 * 4;  // blocks of threads that run at a time
+constexpr int kNear = 1024;     // entries of the plan's tables of lists that are kept in shared memory too
+constexpr int kNearCost = 4096; // ... and of blocks
 constexpr int kBlockCost = 3;   // cost units (tiles) of starting a block, as in the staged prefill
+constexpr int kMergeCost = 6;   // ... of writing and merging the fragments of cut blocks
 
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + kChunkKeys - 1) / kChunkKeys; }
 __device__ __forceinline__ int key_halves(int keys) { return (keys + kHalfKeys - 1) / kHalfKeys; }
@@ -117,12 +119,12 @@ template <int kSpan>
 __device__ void plan(const ChunkParams& p) {
   __shared__ long long part[kStageThreads / 32];
   __shared__ int near_first[kNear], near_own[kNear];
-  __shared__ long long near_cost[kNear];
+  __shared__ long long near_cost[kNearCost];
   const Scan scan{part};
   const int lists = kSpan == kShared ? p.groups : p.batch;
   auto first_of = [&](int b) { return b < kNear ? near_first[b] : p.first_block[b]; };
   auto own_before = [&](int b) { return b < kNear ? near_own[b] : p.own_halves[b]; };
-  auto cost_of = [&](int i) { return i < kNear ? near_cost[i] : p.blocks[i].cost0; };
+  auto cost_of = [&](int i) { return i < kNearCost ? near_cost[i] : p.blocks[i].cost0; };
   // The first token of request b (kShared: its place among the queries).
   auto token_of = [&](int b) { return p.qo_indptr ? clamped(p.qo_indptr, b, p.total_q) : b; };
   long long run = 0, total;
@@ -171,54 +173,73 @@ __device__ void plan(const ChunkParams& p) {
   // Offsets that overlap could name more blocks than there is room for, even more than an int holds.
   const int nblocks = (int)min(run, (long long)p.max_blocks);
   __syncthreads();
-  long long cost = 0;
-  for (int base = 0; base < nblocks; base += kStageThreads) {
-    const int i = base + threadIdx.x;
+  auto block_of = [&](int i) {
     ChunkBlock blk{};
-    if (i < nblocks) {
-      const int b = last_at_most(lists, i, first_of);
-      blk.local0 = (i - first_of(b)) * kChunkRows;
-      int row0;
-      const long long rows = rows_of(b, &row0);
-      blk.row0 = row0 + blk.local0;
-      blk.rows = (int)min((long long)kChunkRows, rows - blk.local0);
-      if constexpr (kSpan == kShared) {
-        const int t0 = blk.row0 / p.heads, t1 = (blk.row0 + blk.rows - 1) / p.heads;  // first and last token
-        auto request_of = [&](int t) { return p.qo_indptr ? last_at_most(p.batch, t, token_of) : t; };
-        const int lo = request_of(t0), hi = max(lo, request_of(t1));
-        const SpanReq r = load_request(p, hi);
-        const int seen = min(r.kv_len, r.kv_len - r.q_len + 1 + t1 - r.q0);
-        const int k0 = clamped(p.prefix_indptr, b, p.num_prefix);
-        blk.head = key_halves(max(clamped(p.prefix_indptr, b + 1, p.num_prefix), k0) - k0);
-        blk.tile0 = prefix_tile0(p, b) * kChunkKeys;
-        // (offsets that overlap could name more halves than there is room for)
-        const int before = min(own_before(lo), own_room(p)), own = max(0, own_before(hi) - own_before(lo));
-        blk.rest0 = p.prefix_tiles * kChunkKeys + before * kHalfKeys;
-        blk.halves = blk.head + min(own + min(key_halves(max(seen, 0)), own_halves(r)), own_room(p) - before);
-      } else {
-        const SpanReq r = load_request(p, b);
-        blk.seen = r.kv_len - r.q_len + 1;
-        const int first = blk.seen + blk.local0 / p.heads, last = blk.seen + (blk.local0 + blk.rows - 1) / p.heads;
-        const StagedKeys all = staged_keys(p, blk.seen);
-        blk.rest_key = window_key(p, first);
-        blk.head = key_halves(min(p.sinks, blk.rest_key));
-        blk.tile0 = request_tile0(p, b) * kChunkKeys;
-        blk.rest0 = blk.tile0 + all.head * kHalfKeys + blk.rest_key - all.low;
-        blk.halves = blk.head + key_halves(max(0, last - blk.rest_key));
-      }
-      blk.tiles = max(1, (blk.halves + 1) / 2);
+    const int b = last_at_most(lists, i, first_of);
+    blk.local0 = (i - first_of(b)) * kChunkRows;
+    int row0;
+    const long long rows = rows_of(b, &row0);
+    blk.row0 = row0 + blk.local0;
+    blk.rows = (int)min((long long)kChunkRows, rows - blk.local0);
+    if constexpr (kSpan == kShared) {
+      const int t0 = blk.row0 / p.heads, t1 = (blk.row0 + blk.rows - 1) / p.heads;  // first and last token
+      auto request_of = [&](int t) { return p.qo_indptr ? last_at_most(p.batch, t, token_of) : t; };
+      const int lo = request_of(t0), hi = max(lo, request_of(t1));
+      const SpanReq r = load_request(p, hi);
+      const int seen = min(r.kv_len, r.kv_len - r.q_len + 1 + t1 - r.q0);
+      const int k0 = clamped(p.prefix_indptr, b, p.num_prefix);
+      blk.head = key_halves(max(clamped(p.prefix_indptr, b + 1, p.num_prefix), k0) - k0);
+      blk.tile0 = prefix_tile0(p, b) * kChunkKeys;
+      // (offsets that overlap could name more halves than there is room for)
+      const int before = min(own_before(lo), own_room(p)), own = max(0, own_before(hi) - own_before(lo));
+      blk.rest0 = p.prefix_tiles * kChunkKeys + before * kHalfKeys;
+      blk.halves = blk.head + min(own + min(key_halves(max(seen, 0)), own_halves(r)), own_room(p) - before);
+    } else {
+      const SpanReq r = load_request(p, b);
+      blk.seen = r.kv_len - r.q_len + 1;
+      const int first = blk.seen + blk.local0 / p.heads, last = blk.seen + (blk.local0 + blk.rows - 1) / p.heads;
+      const StagedKeys all = staged_keys(p, blk.seen);
+      blk.rest_key = window_key(p, first);
+      blk.head = key_halves(min(p.sinks, blk.rest_key));
+      blk.tile0 = request_tile0(p, b) * kChunkKeys;
+      blk.rest0 = blk.tile0 + all.head * kHalfKeys + blk.rest_key - all.low;
+      blk.halves = blk.head + key_halves(max(0, last - blk.rest_key));
     }
-    blk.cost0 = cost + scan(i < nblocks ? blk.tiles + kBlockCost : 0, &total);
-    if (i < nblocks) {
-      p.blocks[i] = blk;
-      if (i < kNear) near_cost[i] = blk.cost0;
+    blk.tiles = max(1, (blk.halves + 1) / 2);
+    return blk;
+  };
+  long long cost = 0;
+  int largest = 0;
+  constexpr int kEach = 4;  // blocks of a thread between two sums
+  for (int base = 0; base < nblocks; base += kStageThreads * kEach) {
+    ChunkBlock blk[kEach];
+    long long own = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = base + threadIdx.x * kEach + e;
+      if (i >= nblocks) continue;
+      blk[e] = block_of(i);
+      blk[e].cost0 = own;
+      own += blk[e].tiles + kBlockCost;
+      largest = max(largest, blk[e].tiles + kBlockCost);
+    }
+    const long long before = cost + scan(own, &total);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = base + threadIdx.x * kEach + e;
+      if (i >= nblocks) continue;
+      blk[e].cost0 += before;
+      p.blocks[i] = blk[e];
+      if (i < kNearCost) near_cost[i] = blk[e].cost0;
     }
     cost += total;
   }
-  __syncthreads();
   // At most one worker for each cost unit, so that two starts inside a block are never the same.
   const long long G = min((long long)p.workers, max(cost, 1LL));
-  auto start_of = [&](long long w) { return w < G ? w * cost / G : cost; };
+  // A worker to each block, if there are enough and the largest block is not far above a worker's share:
+  // then no block is cut, and none has to be merged.
+  const bool uncut = __syncthreads_and(nblocks <= G && largest <= cost / G + kMergeCost);
+  auto start_of = [&](long long w) { return uncut ? (w < nblocks ? cost_of((int)w) : cost) : w < G ? w * cost / G : cost; };
   for (int w = threadIdx.x; w <= p.workers; w += kStageThreads) {
     ChunkStart s{nblocks, 0, ChunkBlock{}};
     ChunkMerge m{0, 0, 0, 0};
@@ -410,24 +431,27 @@ struct StagedRows {
   }
 };
 
-// kTok tokens of a warp on their way from the cache.  A lane has latent values 8 lane .. + 7 and
-// 256 + 8 lane .. + 7, and rope values 8 lane .. + 7.
+// kTok (4 or 8) tokens of a warp on their way from the cache.  A lane has latent values 8 lane .. + 7 and
+// 256 + 8 lane .. + 7 of each, and rope values 8 (lane % 8) .. + 7 of token lane / 8 of each four.
 template <bool kFp8, int kTok>
 struct Tokens {
-  uint4 lat[kFp8 ? 1 : kTok][2], rope[kTok];
+  uint4 lat[kFp8 ? 1 : kTok][2], rope[kTok / 4];
   uint2 code[kFp8 ? kTok : 1][2];
   float scale[kFp8 ? kTok : 1][2];
 
   // Ask for the tokens in slots `mine` of lanes first .. first + kTok - 1 (outside the cache: zeros).
   __device__ __forceinline__ void ask(const ChunkParams& p, int mine, int first) {
     const int lane = threadIdx.x & 31;
+    auto slot_of = [&](int k) {
+      const int s = __shfl_sync(0xffffffffu, mine, first + k);
+      return s < p.num_slots ? s : -1;
+    };
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
-      const int slot = __shfl_sync(0xffffffffu, mine, first + k);
-      rope[k] = make_uint4(0, 0, 0, 0);
+      const int slot = slot_of(k);
       if constexpr (kFp8) code[k][0] = code[k][1] = make_uint2(0, 0), scale[k][0] = scale[k][1] = 0.f;
       else lat[k][0] = lat[k][1] = make_uint4(0, 0, 0, 0);
-      if (slot < 0 || slot >= p.num_slots) continue;
+      if (slot < 0) continue;
       if constexpr (kFp8) {
         const uint8_t* tok = p.kv_fp8 + (size_t)slot * kFp8TokenBytes;
 #pragma unroll
@@ -435,21 +459,37 @@ struct Tokens {
           code[k][h] = *reinterpret_cast<const uint2*>(tok + 256 * h + 8 * lane);
           scale[k][h] = *reinterpret_cast<const float*>(tok + kDimCkv + 8 * h + 4 * (lane >> 4));
         }
-        if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(tok + kDimCkv + 16 + 16 * lane);
       } else {
         const uint4* tok = reinterpret_cast<const uint4*>(p.ckv_cache + (size_t)slot * kDimCkv);
         lat[k][0] = tok[lane];
         lat[k][1] = tok[32 + lane];
-        if (lane < 8) rope[k] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * lane);
       }
     }
+#pragma unroll
+    for (int i = 0; i < kTok / 4; ++i) {
+      const int slot = slot_of(4 * i + (lane >> 3));
+      rope[i] = make_uint4(0, 0, 0, 0);
+      if (slot < 0) continue;
+      if constexpr (kFp8) rope[i] = *reinterpret_cast<const uint4*>(p.kv_fp8 + (size_t)slot * kFp8TokenBytes + kDimCkv + 16 + 16 * (lane & 7));
+      else rope[i] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * (lane & 7));
+    }
+  }
+  // Exponents of all ones among eight bf16 numbers.
+  static __device__ __forceinline__ uint32_t odd_of(uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) odd |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);
+    return odd;
   }
   // Write them to staged rows `row` .. + kTok - 1.  Returns, to all lanes, which of them hold a value that
   // is not finite (their values are written as zeros, so that a weight of zero always makes a
   // zero product).
   __device__ __forceinline__ uint32_t write(const ChunkParams& p, size_t row) {
     const int lane = threadIdx.x & 31;
-    uint32_t bad = 0;
+    uint32_t rope_odd[kTok / 4], bad = 0;
+#pragma unroll
+    for (int i = 0; i < kTok / 4; ++i) rope_odd[i] = __ballot_sync(0xffffffffu, odd_of(rope[i]) != 0);
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
       uint4 a, b;
@@ -460,19 +500,18 @@ struct Tokens {
         a = lat[k][0];
         b = lat[k][1];
       }
-      const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, rope[k].x, rope[k].y, rope[k].z, rope[k].w};
-      uint32_t odd = 0;
-#pragma unroll
-      for (int i = 0; i < 12; ++i) odd |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);  // exponent all ones
-      if (__any_sync(0xffffffffu, odd != 0)) {
-        a = b = rope[k] = make_uint4(0, 0, 0, 0);
+      if (__any_sync(0xffffffffu, (odd_of(a) | odd_of(b)) != 0) || (rope_odd[k / 4] >> (8 * (k & 3)) & 0xffu)) {
+        a = b = make_uint4(0, 0, 0, 0);
         bad |= 1u << k;
       }
       uint4* dst = reinterpret_cast<uint4*>(p.ckv + (row + k) * kDimCkv);
       dst[lane] = a;
       dst[32 + lane] = b;
-      if (lane < 8) *reinterpret_cast<uint4*>(p.kpe + (row + k) * kDimKpe + 8 * lane) = rope[k];
     }
+#pragma unroll
+    for (int i = 0; i < kTok / 4; ++i)
+      reinterpret_cast<uint4*>(p.kpe + (row + 4 * i) * kDimKpe)[lane] =
+          bad >> (4 * i + (lane >> 3)) & 1u ? make_uint4(0, 0, 0, 0) : rope[i];
     return bad;
   }
 };
@@ -482,11 +521,11 @@ struct Tokens {
 // keys and slots outside the cache are written as zeros; the flags tell which rows are keys and
 // which of them were not finite.
 //
-// What bounds it: round trips.  A warp has four tokens on their way, and asks for its next rows'
-// slots meanwhile; with 32 rows to a block of threads, all of whose warps waited for one another,
-// 89K FP8 keys took 34 us.
+// What bounds it: few keys, the chain of round trips (offsets, slots, tokens, the store): a warp asks
+// for its next rows' slots while its tokens are on their way.  Many keys, memory: 158K FP8 keys
+// (285 MB read and written) take 46 us, 6.2 TB/s.  (FP8 tokens eight at a time instead of four: 2 us more, by registers.)
 template <bool kFp8, int kSpan>
-__global__ void __launch_bounds__(kStageThreads, 3) span_stage_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kStageThreads, kFp8 ? 3 : 2) span_stage_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) {
     plan<kSpan>(p);
@@ -512,13 +551,16 @@ __global__ void __launch_bounds__(kStageThreads, 3) span_stage_kernel(const Chun
   if (unit < units) look(unit);
   for (; unit < units; unit += warps) {
     row = next_row, mine = next_mine, used = next_used;
-    Tokens<kFp8, kStageRows / 2> x;
+    constexpr int kTok = kFp8 ? kStageRows / 2 : kStageRows;
+    Tokens<kFp8, kTok> x;
     if (used) x.ask(p, mine, 0);
     if (unit + warps < units) look(unit + warps);
     if (!used) continue;
     uint32_t bad = x.write(p, row);
-    x.ask(p, mine, kStageRows / 2);
-    bad |= x.write(p, (size_t)row + kStageRows / 2) << (kStageRows / 2);
+    if (kTok < kStageRows) {
+      x.ask(p, mine, kTok);
+      bad |= x.write(p, (size_t)row + kTok) << kTok;
+    }
     const uint32_t keys = __ballot_sync(0xffffffffu, mine >= 0 && mine < p.num_slots);
     if (lane == 0) {  // (a byte has the flags of 8 rows)
       reinterpret_cast<uint8_t*>(p.flags)[row / kStageRows] = (uint8_t)keys;
@@ -544,9 +586,11 @@ __global__ void __launch_bounds__(kStageThreads, 4) span_source_kernel(const Chu
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const StagedRows<kSpan> staged(p, &own);
   const int halves = staged.rows / kHalfKeys;
-  for (int first = (blockIdx.x - 1) * halves_per_block; first < halves; first += (gridDim.x - 1) * halves_per_block) {
+  // A block's halves lie far from one another: those to be copied, at a list's ends, are neighbours.
+  const int blocks = gridDim.x - 1;
+  for (int first = blockIdx.x - 1; first < halves; first += blocks * halves_per_block) {
     int copy_row = -1;
-    const int nth = first + warp;
+    const int nth = first + warp * blocks;
     if (warp < halves_per_block && nth < halves) {
       int row;
       RowSource src;
@@ -625,15 +669,16 @@ cudaError_t launch_validate_groups(const ChunkParams& p, cudaStream_t stream) {
 
 cudaError_t launch_span_stage(const ChunkParams& p, int span, bool fp8, cudaStream_t stream) {
   if (p.sources) {
-    // One half a block while they fit a wave, so that copies start at once; else a warp each.
-    const int halves = p.tiles * 2, each = halves <= kSourceBlocks ? 1 : kStageThreads / 32;
+    // As few halves to a block as fill the GPU, and a warp each at most.
+    const int halves = p.tiles * 2, most = kStageThreads / 32;
+    const int each = halves <= kSourceBlocks ? 1 : halves <= kSourceBlocks * most ? (halves + kSourceBlocks - 1) / kSourceBlocks : most;
     const int blocks = (halves + each - 1) / each, grid = 1 + (blocks < kSourceBlocks ? blocks : kSourceBlocks);
     if (span == kWindow) span_source_kernel<kWindow><<<grid, kStageThreads, 0, stream>>>(p, each);
     else span_source_kernel<kShared><<<grid, kStageThreads, 0, stream>>>(p, each);
     return cudaGetLastError();
   }
   const int blocks = (p.tiles * (kChunkKeys / kStageRows) + kStageThreads / 32 - 1) / (kStageThreads / 32);
-  const int grid = 1 + (blocks < kStageBlocks ? blocks : kStageBlocks);
+  const int most = fp8 ? kFp8Blocks : kStageBlocks, grid = 1 + (blocks < most ? blocks : most);
   if (span == kWindow) {
     if (fp8) span_stage_kernel<true, kWindow><<<grid, kStageThreads, 0, stream>>>(p);
     else span_stage_kernel<false, kWindow><<<grid, kStageThreads, 0, stream>>>(p);

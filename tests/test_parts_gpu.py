@@ -182,6 +182,24 @@ def test_split_counts(lib, kind, heads, workers):
     close(call(lib, kind, on_gpu(x), True, args, num_workers=workers), ref)
 
 
+@pytest.mark.parametrize("kind", ["window", "shared"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,page", [(16, 16), (16, 64), (128, 64)])
+@pytest.mark.parametrize("workers", [1, 2, 7])
+def test_many_blocks_to_a_worker(lib, kind, fp8, heads, page, workers):
+    """Decode with few workers: a worker walks through several blocks of several tiles each."""
+    require_gpu()
+    lens = [700, 1, 0, 300, 129, 64, 500, 65, 900, 128, 640, 7]
+    if kind == "window":
+        x, args = make_window([1] * len(lens), lens, heads, page, workers, fp8), (500, 3)
+    else:
+        members = [(1, n) for n in lens]
+        x, args = make_shared([(700, members[:5]), (0, members[5:7]), (130, members[7:])], heads, page, workers, fp8), ()
+    ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    close(call(lib, kind, on_gpu(x), False, args, num_workers=workers, workspace=ws), plain(x, *args))
+    assert lib.read_device_status(ws) == 0
+
+
 # ---------------------------------------------------------------- shared prefixes
 GROUPS = [
     [(300, [(1, 5), (1, 1), (1, 130), (1, 0)])],
@@ -308,6 +326,41 @@ def test_shared_keys_that_are_not_finite(lib, heads, prefill):
     assert torch.isnan(lse[bad]).all() and torch.isnan(out[bad]).all()
     good = ~bad.numpy()
     close((out[~bad], lse[~bad]), tuple(t[good] for t in clean))
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_fp8_keys_that_are_not_finite(lib, heads):
+    """One token per request over an FP8 cache: NaN codes, infinite and NaN scales and rope values spoil
+    the rows that see them alone, whether in the latent's first or last columns or in the rope part."""
+    require_gpu()
+    inf = torch.tensor([float("inf")]).view(torch.uint8)
+
+    def spoil(tokens, slots):
+        tokens[slots[0], 3] = 0x7F
+        tokens[slots[1], 500] = 0xFF
+        tokens[slots[2], 512 + 12:512 + 16] = inf
+        tokens[slots[3], 512:516] = torch.tensor([float("nan")]).view(torch.uint8)
+        tokens[slots[4], 528 + 20:528 + 22] = torch.tensor([float("-inf")], dtype=torch.bfloat16).view(torch.uint8)
+
+    lens = [400, 300, 64, 100, 90, 200, 150]
+    x = make_window([1] * 7, lens, heads, 16, 33, True)
+    ref = plain(x, 60, 10)
+    key = lambda b, t: int(x["ki"][x["kp"][b] + t])  # noqa: E731
+    tokens = x["kv"].view(-1, 656)
+    spoil(tokens, [key(0, t) for t in (10, 100, 200, 300, 339)])            # in front of the window, no sinks
+    spoil(tokens, [key(1, 299), key(2, 3), key(3, 60), key(4, 30), key(5, 9)])  # the last, a sink, in the window
+    out, lse = (t.float().cpu() for t in call(lib, "window", on_gpu(x), False, (60, 10)))
+    bad = torch.tensor([False, True, True, True, True, True, False])
+    assert torch.isnan(lse[bad]).all() and torch.isnan(out[bad]).all()
+    close((out[~bad], lse[~bad]), tuple(t[~bad.numpy()] for t in ref))
+    x = make_shared([(200, [(1, n) for n in (60, 130, 9, 70, 64, 100)]), (70, [(1, 64), (1, 3)])], heads, 16, 34, True)
+    ref = plain(x)
+    tokens, first = x["kv"].view(-1, 656), x["kp"].tolist()
+    spoil(tokens, [int(x["ki"][first[b] + t]) for b, t in ((0, 59), (1, 0), (2, 8), (3, 64), (6, 63))])
+    out, lse = (t.float().cpu() for t in call(lib, "shared", on_gpu(x), False, ()))
+    bad = torch.tensor([True, True, True, True, False, False, True, False])
+    assert torch.isnan(lse[bad]).all() and torch.isnan(out[bad]).all()
+    close((out[~bad], lse[~bad]), tuple(t[~bad.numpy()] for t in ref))
 
 
 @pytest.mark.parametrize("fp8", [False, True])

@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           commit2(issue, bar(g < kKGroups - 1 ? K_EMPTY + g : S_FULL + (j & 1)));
         }
       };
-      auto output = [&](uint32_t j, bool first, uint32_t seg) {  // O += P V of tile j
+      auto output = [&](uint32_t j, bool first, uint32_t seg, bool lone) {  // O += P V of tile j (lone: of its first half)
         wait(P_FULL, j & 1);
         if (first && seg > 0) wait(O_EMPTY, (seg - 1) & 1);
 #pragma unroll
@@ -337,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (uint32_t n = 0; n < 2; ++n)
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
-              mma2(issue, kColO + 128 * n, p0 + h * (kBox / 16) + 2 * k, v0 + (2 * h + n) * (2 * kBox / 16) + 128 * k,
+              mma2(kSpan != kCausal && h > 0 && lone ? 0u : issue, kColO + 128 * n, p0 + h * (kBox / 16) + 2 * k, v0 + (2 * h + n) * (2 * kBox / 16) + 128 * k,
                    kIdescO, h > 0 || k > 0 ? 1u : first ? 0u : 1u);
           commit2(issue, bar(h ? PV_DONE : V_EMPTY));
         }
@@ -347,10 +347,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t j = 0;
       for (Walk it(p, w); it.live && __all_sync(0xffffffffu, good); it.next_segment()) {
         const uint32_t n = it.t_end - it.t;
+        const bool odd = kSpan != kCausal && it.t_end == it.blk.tiles && (it.blk.halves & 1);
         wait(Q_FULL, it.seg & 1);
         for (uint32_t i = 0; i <= n; ++i) {
           if (i < n) scores(j + i);
-          if (i > 0) output(j + i - 1, i == 1, it.seg);
+          if (i > 0) output(j + i - 1, i == 1, it.seg, odd && i == n);
           if (!__all_sync(0xffffffffu, good)) break;
         }
         j += n;

@@ -11,7 +11,9 @@
 // list i: the slots behind them of row i.  Three launches; integer work, whose outcome is unique.
 //
 // What bounds it: latency.  The first launch reads the table once (a block a row), the second is
-// one block's four scans, the third writes the lists.
+// one block's four scans, the third writes the lists: 8 us in a graph for 16 rows of 60 pages, 15 for 500 rows of up to
+// 290, of which 4 MB of lists take 8.  A small table takes one block and one launch (see
+// small_tables_kernel).
 #include "launch.h"
 
 namespace mla {
@@ -173,6 +175,78 @@ __global__ void __launch_bounds__(kThreads) lists_kernel(const SharedTableParams
   }
 }
 
+// A small table in one block: a warp a row.  Two launches less are 5 us of a host's time; lists of more
+// than 64K entries would take one block longer than that.
+constexpr int kSmallRows = 64;
+constexpr long long kSmallKeys = 1 << 16;
+
+__global__ void __launch_bounds__(kScanThreads) small_tables_kernel(const SharedTableParams p) {
+  __shared__ int pages[kSmallRows], group[kSmallRows], opens[kSmallRows + 1], prefix[kSmallRows + 1], own[kSmallRows + 1];
+  const int n = p.batch, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = kScanThreads / 32;
+  for (int i = warp; i < n; i += kWarps) {
+    int differ = i > 0 ? (int)(min(length_of(p, i - 1), length_of(p, i)) / p.page_size) : 0;
+    const int32_t* a = p.block_table + (size_t)i * p.max_blocks;
+    const int most = differ;
+    for (int k = lane; k < most; k += 32)
+      if (__ldg(a + k) != __ldg(a + k - p.max_blocks)) differ = min(differ, k);
+    differ = __reduce_min_sync(0xffffffffu, differ);
+    if (lane == 0) {
+      pages[i] = differ;
+      own[i] = (int)length_of(p, i);  // (at most kSmallKeys)
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const long long least = p.min_shared > 1 ? p.min_shared : 1;
+    int g = -1;
+    for (int i = 0; i < n; ++i) {
+      if (i == 0 || (long long)pages[i] * p.page_size < least) {
+        opens[++g] = i;
+        prefix[g] = -1;
+      } else {
+        prefix[g] = prefix[g] < 0 ? pages[i] : min(prefix[g], pages[i]);
+      }
+      group[i] = g;
+    }
+    int at = 0, next = 0;
+    for (int i = 0; i <= g; ++i) {  // (the least pages become the offsets of the prefixes)
+      const int keys = max(prefix[i], 0) * p.page_size;
+      prefix[i] = at;
+      at += keys;
+    }
+    for (int i = g + 1; i <= n; ++i) opens[i] = n, prefix[i] = at;
+    for (int i = 0; i < n; ++i) {
+      const int keys = own[i] - (prefix[group[i] + 1] - prefix[group[i]]);
+      own[i] = next;
+      next += keys;
+    }
+    own[n] = next;
+  }
+  __syncthreads();
+  if (threadIdx.x <= n) {
+    p.group_indptr[threadIdx.x] = opens[threadIdx.x];
+    p.prefix_indptr[threadIdx.x] = prefix[threadIdx.x];
+    p.kv_indptr[threadIdx.x] = own[threadIdx.x];
+  }
+  auto fill = [&](const int32_t* row, int skip, int from, int to, int32_t* list, long long room) {
+    for (int at = from + lane; at < min((long long)to, room); at += 32) {
+      const int key = skip + at - from;
+      const long long slot = (long long)__ldg(row + key / p.page_size) * p.page_size + key % p.page_size;
+      list[at] = slot < 0 || slot > 0x7fffffffLL ? -1 : (int32_t)slot;
+    }
+  };
+  for (int i = warp; i < 2 * n; i += kWarps) {
+    if (i < n) {
+      const int shared = prefix[group[i] + 1] - prefix[group[i]];
+      fill(p.block_table + (size_t)i * p.max_blocks, shared, own[i], own[i + 1], p.kv_indices, p.capacity);
+    } else if (opens[i - n] < n) {
+      fill(p.block_table + (size_t)opens[i - n] * p.max_blocks, 0, prefix[i - n], prefix[i - n + 1], p.prefix_indices,
+           p.prefix_capacity);
+    }
+  }
+}
+
 template <typename Kernel>
 cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, const SharedTableParams& p, cudaStream_t stream) {
   // A programmatic dependent: its launch overlaps the tail of the one before.
@@ -192,6 +266,10 @@ cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, const SharedTabl
 }  // namespace
 
 cudaError_t launch_shared_tables(const SharedTableParams& p, cudaStream_t stream) {
+  if (p.batch <= kSmallRows && (long long)p.batch * p.max_blocks * p.page_size <= kSmallKeys) {
+    small_tables_kernel<<<1, kScanThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
   const int rows = p.batch < 65535 ? (p.batch > 0 ? p.batch : 1) : 65535;
   common_pages_kernel<<<rows, kThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();

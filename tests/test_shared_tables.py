@@ -94,7 +94,8 @@ def random_table(rng, n, blocks, page, share, ids=50):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("n,blocks", [(1, 1), (2, 3), (33, 7), (100, 300), (1023, 4), (1025, 5), (2500, 3)])
+@pytest.mark.parametrize("n,blocks", [(1, 1), (2, 3), (33, 7), (64, 16), (64, 17), (65, 2), (100, 300), (1023, 4), (1025, 5),
+                                      (2500, 3)])
 @pytest.mark.parametrize("page", [1, 16, 64])
 def test_tables_equal_the_oracle(lib, n, blocks, page):
     require_gpu()

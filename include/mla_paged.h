@@ -300,10 +300,10 @@ int mla_paged_prefill_fp8(const void* q_nope, const void* q_pe, const void* kv_f
  * slot outside the cache is not a key; a key with a value that is not finite makes out and lse
  * NaN in the rows that see it and changes no other row.
  *   workspace >= mla_workspace_bytes_window(dims, window, sinks, is_prefill) bytes (is_prefill:
- *   1 for the prefill calls), zero-filled before its first use.  It holds a copy of the keys
- *   seen: 1152 bytes a key, in whole tiles of 128 for at most min(num_kv_indices + 127 per
- *   request, total_q + (window + sinks + 510) per request) keys.  Calls whose staged keys would number 2^31 or more are
- *   refused (MLA_ERR_DIMS; their workspace size reads 0).
+ *   1 for the prefill calls), zero-filled before its first use.  It has room for a copy of the keys
+ *   seen: 1152 bytes a key, in tiles of 128, for the fewer of num_kv_indices + 128 per request
+ *   and total_q + (window + sinks + 510) per request.  Calls whose staged keys would number 2^31
+ *   or more are refused (MLA_ERR_DIMS; their workspace size reads 0).
  * The _fp8 calls read the FP8 cache of mla_paged_decode_fp8.
  */
 size_t mla_workspace_bytes_window(const mla_dims* dims, int window, int sinks, int is_prefill);
@@ -343,7 +343,9 @@ int mla_paged_prefill_window_fp8(const void* q_nope, const void* q_pe, const voi
  *   dims->num_kv_indices, and up to 128 keys per group and request.  Staged keys of 2^31 or more are
  *   refused (MLA_ERR_DIMS; their workspace size reads 0).
  * Empty rows, rows behind the last request, slots outside the cache and keys that are not finite:
- * as for mla_paged_prefill_window.  MLA_VALIDATE checks both lists and the groups.
+ * as for mla_paged_prefill_window.  MLA_VALIDATE checks both lists and the groups; as in the
+ * other calls it reports lists that end short of their capacity, and for the prefill calls
+ * requests with fewer own keys than new tokens, which are no error otherwise.
  * The _fp8 calls read the FP8 cache of mla_paged_decode_fp8.
  */
 size_t mla_workspace_bytes_shared(const mla_dims* dims, int groups, int num_prefix_indices, int is_prefill);
@@ -382,7 +384,8 @@ int mla_paged_prefill_shared_fp8(const void* q_nope, const void* q_pe, const voi
  *   kv_indptr [batch + 1], kv_indices [capacity]: every row's keys behind the shared ones
  * Slots as for mla_block_table_to_csr (-1 where they do not fit an int32).  Entries at or past a
  * capacity, and behind the end of a list, are left as they were; the offsets still count
- * entries past the capacity, and stay at 2^31 - 1 once they have reached it.  Three launches.
+ * entries past the capacity, and stay at 2^31 - 1 once they have reached it.  Three launches, or
+ * one for up to 64 rows with 65,536 keys at most (batch * max_blocks * page_size).
  * For a step with several new tokens per row call it after the pool has been extended: pages
  * with new tokens are never shared.
  * MLA_ERR_DIMS: negative sizes, page_size < 1, max_blocks * page_size or a capacity above

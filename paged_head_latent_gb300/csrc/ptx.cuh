@@ -103,21 +103,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// The same in less code (a quarter of it where it is inlined), for a kernel whose loops have to share
-// the instruction cache.  Times are in units of 1024 ns.
-__device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status,
-                                                uint32_t timeout_bit, uint32_t limit) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint32_t t0 = static_cast<uint32_t>(globaltimer() >> 10);
-#pragma unroll 1
-  do {
-    if (mbar_try_wait(bar, parity)) return true;
-  } while (!*abort && static_cast<uint32_t>(globaltimer() >> 10) - t0 <= limit);
-  if (!*abort) atomicOr(status, timeout_bit);
-  *abort = 1;
-  return false;
-}
-
 // ---------------------------------------------------------------- fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

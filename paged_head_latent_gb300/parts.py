@@ -51,7 +51,8 @@ def _attend(name, q_nope, q_pe, cache, qo_indptr, ints, kv_indptr, kv_indices, m
     index = q_nope.get_device()
     shape = q_nope.shape
     fp8 = len(cache) == 1
-    if not (_good(index, _BF16, q_pe, *(() if fp8 else cache)) and _good(index, _I32, kv_indptr, kv_indices, *ints.values())
+    if not (_good(index, _BF16, q_pe, *(() if fp8 else cache))
+            and _good(index, _I32, kv_indptr, kv_indices, *ints.values())
             and (not fp8 or _good(index, _U8, *cache)) and (qo_indptr is None or _good(index, _I32, qo_indptr))):
         _check("q_pe", q_pe, _BF16, index)
         for n, t in zip(("kv_fp8",) if fp8 else ("ckv_cache", "kpe_cache"), cache):
@@ -70,6 +71,8 @@ def _attend(name, q_nope, q_pe, cache, qo_indptr, ints, kv_indptr, kv_indices, m
     if batch < 0:
         raise ValueError("kv_indptr must have batch + 1 entries")
     if qo_indptr is None:
+        if "prefill" in name:
+            raise TypeError("qo_indptr must be a torch.Tensor")
         if rows != batch:
             raise ValueError("decode: q_nope.shape[0] must equal len(kv_indptr) - 1")
         first = ()
@@ -77,7 +80,8 @@ def _attend(name, q_nope, q_pe, cache, qo_indptr, ints, kv_indptr, kv_indices, m
         if qo_indptr.numel() != batch + 1:
             raise ValueError("qo_indptr and kv_indptr must both have batch + 1 entries")
         first = (qo_indptr.data_ptr(),)
-    dims = MlaDims(batch, heads, HEAD_DIM_CKV, HEAD_DIM_KPE, num_pages, page_size, rows, kv_indices.numel(), num_workers)
+    dims = MlaDims(batch, heads, HEAD_DIM_CKV, HEAD_DIM_KPE, num_pages, page_size, rows, kv_indices.numel(),
+                   int(num_workers))
     out = _buffer("out", out, shape, _BF16, q_nope, stream)
     lse = _buffer("lse", lse, (rows, heads), _F32, q_nope, stream)
     if workspace is None:
@@ -87,7 +91,8 @@ def _attend(name, q_nope, q_pe, cache, qo_indptr, ints, kv_indptr, kv_indices, m
     elif not _good(index, _U8, workspace):  # (the library checks its size)
         _check("workspace", workspace, _U8, index)
     _call(name, index, stream, q_nope.data_ptr(), q_pe.data_ptr(), *[t.data_ptr() for t in cache], *first, *middle,
-          sm_scale, out.data_ptr(), lse.data_ptr(), ctypes.byref(dims), workspace.data_ptr(), workspace.numel(), flags)
+          float(sm_scale), out.data_ptr(), lse.data_ptr(), ctypes.byref(dims), workspace.data_ptr(), workspace.numel(),
+          int(flags))
     return out, lse
 
 

@@ -515,3 +515,119 @@ def test_corrupt_offsets_stay_inside_the_buffers(lib, seed):
         assert (out[:11] == 7).all() and (out[22:] == 7).all() and (lse[:11] == 7).all() and (lse[22:] == 7).all()
         assert (ws[need:] == 0x5A).all()
         assert lib.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("page", [16, 64])
+def test_a_workspace_that_other_calls_have_filled(lib, fp8, prefill, page):
+    """Whatever lies behind the status word (here NaN in every type) is written before it is read."""
+    require_gpu()
+    q = ((3, 90), (7, 200), (1, 130), (2, 0)) if prefill else ((1, 90), (1, 200), (1, 130), (1, 0))
+    for kind, x, args in both(24, page, fp8, 21, q):
+        ws = torch.full((1 << 28,), 0xFF, dtype=torch.uint8, device="cuda")
+        ws[:256] = 0
+        close(call(lib, kind, on_gpu(x), prefill, args, workspace=ws), plain(x, *args))
+        assert lib.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_own_pages_that_are_not_finite(lib, heads, prefill):
+    """A NaN key in a whole page of one request's own keys: the group's other requests, whose rows may
+    share a block with that request's, stay as they are."""
+    require_gpu()
+    n = [2, 1, 3] if prefill else [1] * 3
+    for members in ([(n[0], 128), (n[1], 200), (n[2], 70)], [(n[0], 200)]):
+        x = make_shared([(64, members)], heads, 64, 35)
+        clean = plain(x)
+        at = int(x["kp"][int(len(members) > 1)]) + 70  # the second page of the second request, or of the only one
+        x["ckv"].view(-1, 512)[int(x["ki"][at]), 9] = float("nan")
+        out, lse = (t.float().cpu() for t in call(lib, "shared", on_gpu(x), prefill, ()))
+        bad = torch.ones(len(out), dtype=torch.bool)
+        if len(members) > 1:
+            bad[:n[0]] = False
+            bad[n[0] + n[1]:] = False
+        assert torch.isnan(lse[bad]).all() and torch.isnan(out[bad]).all()
+        good = ~bad.numpy()
+        close((out[~bad], lse[~bad]), tuple(t[good] for t in clean))
+
+
+@pytest.mark.parametrize("kind", ["window", "shared", "causal"])
+def test_outputs_on_a_16_byte_boundary(lib, kind):
+    """Rows of the output are written 32 bytes at a time where its address allows it, else 16."""
+    require_gpu()
+    x, args = make_window([3, 40], [150, 40], 16, 16, 41), (2 ** 31 - 1, 0)
+    if kind == "shared":
+        x, args = make_shared([(30, [(3, 50), (40, 70)])], 16, 16, 41), ()
+    c, ref = on_gpu(x), plain(x)
+    for skip in (8, 16):
+        flat = torch.full((43 * 16 * 512 + 32,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = flat[skip:skip + 43 * 16 * 512].view(43, 16, 512)
+        assert out.data_ptr() % 32 == 2 * skip % 32
+        if kind == "causal":
+            got = lib.mla_paged_prefill_staged(c["qn"], c["qp"], c["ckv"], c["kpe"], c["qo"], c["kp"], c["ki"], SCALE,
+                                               out=out)
+        else:
+            got = call(lib, kind, c, True, args, out=out)
+        close(got, ref)
+        assert (flat[:skip] == 7).all() and (flat[skip + 43 * 16 * 512:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["window", "shared"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_bounded_waits(lib, kind, page):
+    """A load that never happens: the call returns, the status says timeout, the next call is right."""
+    require_gpu()
+    if kind == "window":
+        x, args = make_window([1] * 3, [2000, 700, 5], 16, page, 36), (1000, 100)
+    else:
+        x, args = make_shared([(700, [(1, 2000), (1, 5)])], 16, page, 36), ()
+    ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    c = on_gpu(x)
+    try:
+        lib.lib().mla_debug_inject_timeout(1, 20_000_000)
+        call(lib, kind, c, False, args, workspace=ws, num_workers=1)
+        assert lib.read_device_status(ws) == -7
+    finally:
+        lib.lib().mla_debug_inject_timeout(-1, 0)
+    close(call(lib, kind, c, False, args, workspace=ws, num_workers=1), plain(x, *args))
+    assert lib.read_device_status(ws) == 0
+
+
+def test_two_calls_at_once(lib):
+    """On two streams, with a workspace each."""
+    require_gpu()
+    made = [entry for seed in (51, 52) for entry in both(16, 64, False, seed, ((40, 2000), (3, 1000), (1, 5)))]
+    inputs = [on_gpu(x) for _, x, _ in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[call(lib, kind, c, True, args, stream=s) for _ in range(3)][-1]
+           for s, (kind, _, args), c in zip(streams, made, inputs)]
+    torch.cuda.synchronize()
+    for g, (kind, x, args) in zip(got, made):
+        close(g, plain(x, *args))
+
+
+def test_far_slots(lib):
+    """Slots past 2^31 bytes of the caches, staged and read where they lie."""
+    require_gpu()
+    pages, page = 36000, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ckv = torch.zeros(pages, page, 512, dtype=torch.bfloat16, device="cuda")
+    kpe = torch.zeros(pages, page, 64, dtype=torch.bfloat16, device="cuda")
+    far = pages - 8
+    ckv[far:].normal_(generator=g)
+    kpe[far:].normal_(generator=g)
+    slots = torch.arange(far * page, pages * page, dtype=torch.int32)
+    x = dict(qn=torch.randn(2, 16, 512, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16),
+             qp=torch.randn(2, 16, 64, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16), qo=offsets([1, 1]))
+    y = dict(x, ki=slots[:431], kp=offsets([300, 131]))
+    z = dict(x, pi=slots[:200], pp=offsets([200]), gp=offsets([2]), ki=slots[200:431], kp=offsets([100, 131]))
+    for kind, v, args in (("window", y, (200, 3)), ("shared", z, ())):
+        got = call(lib, kind, {**on_gpu(v), "ckv": ckv, "kpe": kpe}, False, args)
+        near = {**v, "ckv": ckv[far:].cpu(), "kpe": kpe[far:].cpu()}
+        for name in ("ki", "pi"):
+            if name in near:
+                near[name] = near[name] - far * page
+        close(got, plain(near, *args))

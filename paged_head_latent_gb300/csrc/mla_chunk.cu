@@ -602,7 +602,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive_leader(o_empty);
           }
-          if (in_block + lane >= it.blk.rows) continue;
           float y[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(x[k]) * inv;
@@ -613,16 +612,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
               h[k] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            __nv_bfloat16* dst = p.out + ((size_t)it.blk.row0 + in_block + lane) * kDimCkv + 256 * half + 128 * part + 32 * c;
-            if (wide) {
-              st_global_v8(dst, h);
-              st_global_v8(dst + 16, h + 8);
-            } else {
+            // Two lanes write 64 bytes of a row together, then of the other's row: half the lines to a store.
+            // (Windows of 1024 keys with 128 heads 596 -> 586 us; four lanes and 128 bytes take more
+            // code and registers: 653.)
+            const bool upper = lane & 1;
 #pragma unroll
-              for (int u = 0; u < 4; ++u)
-                reinterpret_cast<uint4*>(dst)[u] = make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? h[k] : h[8 + k], 1);
+              if (upper) h[k] = got; else h[8 + k] = got;
             }
-          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int rr = in_block + (lane & ~1) + i;
+              if (rr >= it.blk.rows) continue;
+              __nv_bfloat16* dst =
+                  p.out + ((size_t)it.blk.row0 + rr) * kDimCkv + 256 * half + 128 * part + 32 * c + 16 * (lane & 1);
+              if (wide) {
+                st_global_v8(dst, h + 8 * i);
+              } else {
+                reinterpret_cast<uint4*>(dst)[0] = make_uint4(h[8 * i], h[8 * i + 1], h[8 * i + 2], h[8 * i + 3]);
+                reinterpret_cast<uint4*>(dst)[1] = make_uint4(h[8 * i + 4], h[8 * i + 5], h[8 * i + 6], h[8 * i + 7]);
+              }
+            }
+          } else if (in_block + lane < it.blk.rows) {
             // A fragment lies as [column / 4][row][4], so a store is 512 contiguous bytes.
             float4* dst = reinterpret_cast<float4*>(p.part_o + frag * kDimCkv) + (64 * half + 32 * part + 8 * c) * kChunkRows +
                           in_block + lane;

@@ -9,6 +9,12 @@ namespace mla {
 
 constexpr int kChunkKeys = 128;  // keys of a tile
 constexpr int kChunkRows = 128;  // query rows (token, head) of a block
+// Cost units (tiles) of starting a block: its Q load and its output.  Four prompts with 128 heads
+// took 935, 881, 871 and 886 us at 1 to 4, 32 blocks of drafted tokens 24.7, 22.9, 22.7 and 23.9.
+constexpr int kBlockCost = 3;
+// ... and, in the window and the shared attention's plan, of writing and merging the fragments of cut
+// blocks; tiles of a block that never pay a cut.
+constexpr int kMergeCost = 6, kUncutTiles = kMergeCost - kBlockCost;
 
 // Which keys a row sees.  kCausal: all of its request's keys up to its own token.  kWindow: of
 // those the last `window` and the first `sinks`.  kShared: all keys of its group's prefix list,
@@ -84,6 +90,7 @@ struct ChunkParams {
   int window, sinks;
   int per_request;      // kWindow: tiles set aside for a request, or 0: for all of its keys
   int aligned;          // kWindow: the second run starts at a multiple of 64 keys (sources, or per_request = 0)
+  bool uncut;           // known to the host: at most as many blocks as workers, of up to kUncutTiles; no merge
   const int32_t* group_indptr;   // [groups + 1] requests
   const int32_t* prefix_indptr;  // [groups + 1] prefix keys
   const int32_t* prefix_indices;

@@ -9,9 +9,6 @@ namespace {
 constexpr int kStageThreads = 256;
 constexpr int kStageKeys = 32;  // keys of a staging block: one word of the tile's flags
 constexpr int kNear = 1024;  // entries of the plan's tables that are kept in shared memory too
-// Cost units (tiles) of starting a block: its Q load and its output.  Four prompts with 128 heads
-// took 935, 881, 871 and 886 us at 1 to 4, 32 blocks of drafted tokens 24.7, 22.9, 22.7 and 23.9.
-constexpr int kBlockCost = 3;
 
 struct ChunkReq {
   int q0, q_len, k0, kv_len;

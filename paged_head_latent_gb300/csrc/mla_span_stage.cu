@@ -17,8 +17,6 @@ constexpr int kStageRows = 8;   // staged rows that a warp takes at a time: one 
 constexpr int kStageBlocks = 152 * 2, kFp8Blocks = 152 * 3, kSourceBlocks = 152 * 4;  // blocks of threads that run at a time
 constexpr int kNear = 1024;     // entries of the plan's tables of lists that are kept in shared memory too
 constexpr int kNearCost = 4096; // ... and of blocks
-constexpr int kBlockCost = 3;   // cost units (tiles) of starting a block, as in the staged prefill
-constexpr int kMergeCost = 6;   // ... of writing and merging the fragments of cut blocks
 
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + kChunkKeys - 1) / kChunkKeys; }
 __device__ __forceinline__ int key_halves(int keys) { return (keys + kHalfKeys - 1) / kHalfKeys; }
@@ -238,7 +236,7 @@ __device__ void plan(const ChunkParams& p) {
   const long long G = min((long long)p.workers, max(cost, 1LL));
   // A worker to each block, if there are enough and the largest block is not far above a worker's share:
   // then no block is cut, and none has to be merged.
-  const bool uncut = __syncthreads_and(nblocks <= G && largest <= cost / G + kMergeCost);
+  const bool uncut = __syncthreads_and(nblocks <= G && (p.uncut || largest <= cost / G + kMergeCost));
   auto start_of = [&](long long w) { return uncut ? (w < nblocks ? cost_of((int)w) : cost) : w < G ? w * cost / G : cost; };
   for (int w = threadIdx.x; w <= p.workers; w += kStageThreads) {
     ChunkStart s{nblocks, 0, ChunkBlock{}};

@@ -82,7 +82,10 @@ def _attend(name, q_nope, q_pe, cache, qo_indptr, ints, kv_indptr, kv_indices, m
         first = (qo_indptr.data_ptr(),)
     dims = MlaDims(batch, heads, HEAD_DIM_CKV, HEAD_DIM_KPE, num_pages, page_size, rows, kv_indices.numel(),
                    int(num_workers))
-    out = _buffer("out", out, shape, _BF16, q_nope, stream)
+    if out is None and stream is None:
+        out = torch.empty_like(q_nope)  # (quicker than by its shape)
+    else:
+        out = _buffer("out", out, shape, _BF16, q_nope, stream)
     lse = _buffer("lse", lse, (rows, heads), _F32, q_nope, stream)
     if workspace is None:
         with torch.cuda.device(index):

@@ -37,8 +37,8 @@
 // bf16 cache (kDirect), and an odd block's last half costs no P V product.  A tile takes as long as a
 // causal one; what else a call costs is starts of blocks (about three tiles each, which short
 // windows and lists have many of).  Measured at the power limit, with staging: 2710 tokens of 128
-// heads with windows of 1024 keys 594 us (1.27 PFLOP/s), 1374 tokens of 128 heads behind two prefixes of
-// 1408 keys 450 us (1.41).  64 requests x 128 heads, windows of 4096 keys in 64-key pages: 82 us, DRAM at
+// heads with windows of 1024 keys 583 us (1.29 PFLOP/s), 1374 tokens of 128 heads behind two prefixes of
+// 1408 keys 448 us (1.42).  64 requests x 128 heads, windows of 4096 keys in 64-key pages: 82 us, DRAM at
 // 4.7 to 4.9 TB/s in the kernel, which starts and ends with no load in flight.
 //
 // The tensor pipe's order is S(j+1), then O += P(j) V(j): the softmax of tile j runs while S(j+1)

@@ -8,12 +8,11 @@
 //   shared_g = page_size * min pages_i over the rows that joined group g; 0 if none did
 // As the leading pages of a row are compared with those of its neighbour, the least of a group is
 // what all its rows share.  prefix list g: the first shared_g slots of the group's first row; own
-// list i: the slots behind them of row i.  Three launches; integer work, whose outcome is unique.
+// list i: the slots behind them of row i.  Integer work, whose outcome is unique.
 //
 // What bounds it: latency.  The first launch reads the table once (a block a row), the second is
-// one block's four scans, the third writes the lists: 8 us in a graph for 16 rows of 60 pages, 15 for 500 rows of up to
-// 290, of which 4 MB of lists take 8.  A small table takes one block and one launch (see
-// small_tables_kernel).
+// one block's four scans, the third writes the lists: 15 us in a graph for 500 rows of up to 290
+// pages, 4, 5 and 10 us by themselves.  A small table takes one block and one launch: 8 us for 16 rows of 60 pages.
 #include "launch.h"
 
 namespace mla {
@@ -175,8 +174,8 @@ __global__ void __launch_bounds__(kThreads) lists_kernel(const SharedTableParams
   }
 }
 
-// A small table in one block: a warp a row.  Two launches less are 5 us of a host's time; lists of more
-// than 64K entries would take one block longer than that.
+// A small table in one block: a warp a row.  16 rows of 60 pages take 16 us a call instead of 24, two
+// launches less of the host's time; lists of more than 64K entries would take one block longer than that.
 constexpr int kSmallRows = 64;
 constexpr long long kSmallKeys = 1 << 16;
 

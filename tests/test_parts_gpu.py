@@ -631,3 +631,67 @@ def test_far_slots(lib):
             if name in near:
                 near[name] = near[name] - far * page
         close(got, plain(near, *args))
+
+
+@pytest.mark.parametrize("kind", ["window", "shared"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_a_million_keys(lib, kind, page):
+    """Staged rows past 1 GB (page 16), a block split over every worker, halves read in place (page 64)."""
+    require_gpu()
+    n, own = 1_100_000, (77, 1)
+    pages = -(-(n + sum(own)) // page) + 2
+    g = torch.Generator(device="cuda").manual_seed(page)
+    ckv = torch.randn(pages, page, 512, generator=g, device="cuda", dtype=torch.bfloat16)
+    kpe = torch.randn(pages, page, 64, generator=g, device="cuda", dtype=torch.bfloat16)
+    at = torch.randperm(pages, generator=g, device="cuda")
+    slots = (at[:, None] * page + torch.arange(page, device="cuda")).view(-1).int()
+    qn = torch.randn(2, 5, 512, generator=g, device="cuda", dtype=torch.bfloat16)
+    qp = torch.randn(2, 5, 64, generator=g, device="cuda", dtype=torch.bfloat16)
+    x = dict(qn=qn, qp=qp, ckv=ckv, kpe=kpe)
+    a, b = slots[:n], slots[n:n + sum(own)]
+    if kind == "shared":
+        x.update(pi=a.contiguous(), pp=offsets([n]).cuda(), gp=offsets([2]).cuda(), ki=b.contiguous(), kp=offsets(own).cuda())
+        lists, args = [torch.cat([a, b[:77]]), torch.cat([a, b[77:]])], ()
+    else:  # the first request sees a window of 1,000,000 and 5 sinks, the second all of its keys
+        x.update(ki=slots[:n + sum(own)].contiguous(), kp=offsets([n, sum(own)]).cuda())
+        lists, args = [torch.cat([a[:5], a[n - 1_000_000:]]), b], (1_000_000, 5)
+    ref = []
+    for r, keys in enumerate(lists):
+        s, w, parts = [], qn[r].double(), keys.long().split(200_000)
+        k = [ckv.view(-1, 512)[i].double() for i in parts]
+        e = [kpe.view(-1, 64)[i].double() for i in parts]
+        s = torch.cat([w @ y.T + qp[r].double() @ z.T for y, z in zip(k, e)], 1) * SCALE
+        size = torch.stack([(w.abs() @ y.abs().T + qp[r].double().abs() @ z.abs().T).amax(-1) for y, z in zip(k, e)]).amax(0)
+        lse = torch.logsumexp(s, -1)
+        p = torch.exp(s - lse[:, None]).split(200_000, 1)
+        ref.append((sum(u @ y for u, y in zip(p, k)), lse, sum(u @ y.abs() for u, y in zip(p, k)), 2.0 ** -14 * SCALE * size))
+    close(call(lib, kind, x, False, args), tuple(torch.stack(t).cpu().numpy() for t in zip(*ref)))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("page", [16, 64])
+def test_lists_without_entries(lib, fp8, prefill, page):
+    """No prefix index, no own index, neither: null pointers on the C side."""
+    require_gpu()
+    n = 3 if prefill else 1
+    close(call(lib, "window", on_gpu(make_window([n, n], [0, 0], 16, page, 1, fp8)), prefill, (5, 2)),
+          plain(make_window([n, n], [0, 0], 16, page, 1, fp8), 5, 2))
+    for groups in ([(0, [(n, 4), (n, 70)]), (0, [(n, 1)])], [(70, [(n, 0), (n, 0)])], [(0, [(n, 0), (n, 0)])]):
+        x = make_shared(groups, 16, page, 2, fp8)
+        assert not x["pi"].numel() or not x["ki"].numel()
+        close(call(lib, "shared", on_gpu(x), prefill, ()), plain(x))
+
+
+@pytest.mark.parametrize("kind", ["window", "shared"])
+def test_a_negative_scale(lib, kind):
+    require_gpu()
+    for x, args in ((make_window([1, 1], [300, 20], 16, 64, 71), (128, 3)),
+                    (make_shared([(200, [(1, 300), (1, 20)])], 16, 64, 71), ())):
+        if ("gp" in x) != (kind == "shared"):
+            continue
+        c = on_gpu(x)
+        got = getattr(lib, f"mla_paged_decode_{kind}")(
+            c["qn"], c["qp"], c["ckv"], c["kpe"],
+            *((c["kp"], c["ki"], *args) if kind == "window" else (c["gp"], c["pp"], c["pi"], c["kp"], c["ki"])), -SCALE)
+        close(got, plain({**x, "qn": -x["qn"], "qp": -x["qp"]}, *args))

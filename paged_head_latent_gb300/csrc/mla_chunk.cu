@@ -27,8 +27,8 @@
 //
 // What bounds it.  A tile takes 2470 cycles with its share of the blocks' starts and ends (four
 // prompts, 128 heads, 22 tiles a block: 850 to 870 us with staging and merge, 1.72 to 1.76 PFLOP/s,
-// 0.90 to 0.92 of the measured bf16 burst rate, at the 1.6 GHz that the power limit leaves; one prompt of 256 tokens over 4096 keys: tensor pipe
-// 80 % active).  What writes shared memory, the loads and P, is 152 KB a tile, 1216 cycles at 128
+// 0.90 to 0.92 of the measured bf16 burst rate, at the 1.6 GHz that the power limit leaves; one
+// prompt of 256 tokens over 4096 keys: tensor pipe 80 % active).  What writes shared memory, the loads and P, is 152 KB a tile, 1216 cycles at 128
 // bytes a cycle; the products read their operands besides, at a rate that was not measured.
 //
 // The window and the shared attention (kSpan; decode calls of theirs too) take the same tiles as
@@ -285,7 +285,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (fault && (int)j == p.fault_skip_tile) break;  // (test of the give-up path: no more loads)
 #pragma unroll
           for (uint32_t g = 0; g < kKGroups; ++g) {
-            if (j > 0 && !(ok = g < kKGroups - 1 ? wait(K_EMPTY + g, again) : wait(S_FULL + again, ((j - 1) >> 1) & 1))) break;
+            if (j > 0 && !(ok = g < kKGroups - 1 ? wait(K_EMPTY + g, again)
+                                                 : wait(S_FULL + again, ((j - 1) >> 1) & 1)))
+              break;
             if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(K_FULL + g), 2 * kGroup * kBox);
             if (group == g) tma_load_pair(dst, map, column, row, full);
           }
@@ -703,8 +705,10 @@ cudaError_t launch_instance(const ChunkMaps& maps, const ChunkParams& p, cudaStr
 
 cudaError_t launch_chunk(const ChunkMaps& maps, const ChunkParams& p, int span, cudaStream_t stream) {
   const bool direct = p.sources != nullptr;
-  if (span == kWindow) return direct ? launch_instance<kWindow, true>(maps, p, stream) : launch_instance<kWindow, false>(maps, p, stream);
-  if (span == kShared) return direct ? launch_instance<kShared, true>(maps, p, stream) : launch_instance<kShared, false>(maps, p, stream);
+  if (span == kWindow)
+    return direct ? launch_instance<kWindow, true>(maps, p, stream) : launch_instance<kWindow, false>(maps, p, stream);
+  if (span == kShared)
+    return direct ? launch_instance<kShared, true>(maps, p, stream) : launch_instance<kShared, false>(maps, p, stream);
   return launch_instance<kCausal, false>(maps, p, stream);
 }
 

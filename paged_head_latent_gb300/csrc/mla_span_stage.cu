@@ -14,7 +14,8 @@ namespace {
 
 constexpr int kStageThreads = 256;
 constexpr int kStageRows = 8;   // staged rows that a warp takes at a time: one byte of the flags
-constexpr int kStageBlocks = 152 * 2, kFp8Blocks = 152 * 3, kSourceBlocks = 152 * 4;  // blocks of threads that run at a time
+// Blocks of threads that run at a time.
+constexpr int kStageBlocks = 152 * 2, kFp8Blocks = 152 * 3, kSourceBlocks = 152 * 4;
 constexpr int kNear = 1024;     // entries of the plan's tables of lists that are kept in shared memory too
 constexpr int kNearCost = 4096; // ... and of blocks
 
@@ -468,8 +469,10 @@ struct Tokens {
       const int slot = slot_of(4 * i + (lane >> 3));
       rope[i] = make_uint4(0, 0, 0, 0);
       if (slot < 0) continue;
-      if constexpr (kFp8) rope[i] = *reinterpret_cast<const uint4*>(p.kv_fp8 + (size_t)slot * kFp8TokenBytes + kDimCkv + 16 + 16 * (lane & 7));
-      else rope[i] = *reinterpret_cast<const uint4*>(p.kpe_cache + (size_t)slot * kDimKpe + 8 * (lane & 7));
+      const uint8_t* part;
+      if constexpr (kFp8) part = p.kv_fp8 + (size_t)slot * kFp8TokenBytes + kDimCkv + 16;
+      else part = reinterpret_cast<const uint8_t*>(p.kpe_cache + (size_t)slot * kDimKpe);
+      rope[i] = reinterpret_cast<const uint4*>(part)[lane & 7];
     }
   }
   // Exponents of all ones among eight bf16 numbers.
@@ -521,7 +524,8 @@ struct Tokens {
 //
 // What bounds it: few keys, the chain of round trips (offsets, slots, tokens, the store): a warp asks
 // for its next rows' slots while its tokens are on their way.  Many keys, memory: 158K FP8 keys
-// (285 MB read and written) take 46 us, 6.2 TB/s.  (FP8 tokens eight at a time instead of four: 2 us more, by registers.)
+// (285 MB read and written) take 46 us, 6.2 TB/s.  (FP8 tokens eight at a time instead of four: 2 us
+// more, by registers.)
 template <bool kFp8, int kSpan>
 __global__ void __launch_bounds__(kStageThreads, kFp8 ? 3 : 2) span_stage_kernel(const ChunkParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -669,7 +673,7 @@ cudaError_t launch_span_stage(const ChunkParams& p, int span, bool fp8, cudaStre
   if (p.sources) {
     // As few halves to a block as fill the GPU, and a warp each at most.
     const int halves = p.tiles * 2, most = kStageThreads / 32;
-    const int each = halves <= kSourceBlocks ? 1 : halves <= kSourceBlocks * most ? (halves + kSourceBlocks - 1) / kSourceBlocks : most;
+    const int each = (int)min(((long long)halves + kSourceBlocks - 1) / kSourceBlocks, (long long)most);
     const int blocks = (halves + each - 1) / each, grid = 1 + (blocks < kSourceBlocks ? blocks : kSourceBlocks);
     if (span == kWindow) span_source_kernel<kWindow><<<grid, kStageThreads, 0, stream>>>(p, each);
     else span_source_kernel<kShared><<<grid, kStageThreads, 0, stream>>>(p, each);

@@ -248,7 +248,7 @@ def block_table_to_shared_csr(block_table, seq_lens, page_size, min_shared=1, pr
     kv_indptr = _buffer("kv_indptr", kv_indptr, (batch + 1,), _I32, block_table, stream)
     prefix_indices = _buffer("prefix_indices", prefix_indices, (prefix_capacity,), _I32, block_table, stream)
     kv_indices = _buffer("kv_indices", kv_indices, (capacity,), _I32, block_table, stream)
-    _call("mla_block_table_to_shared_csr", index, stream, block_table.data_ptr(), seq_lens.data_ptr(), batch, max_blocks,
-          page_size, min_shared, group_indptr.data_ptr(), prefix_indptr.data_ptr(), prefix_indices.data_ptr(), prefix_capacity,
-          kv_indptr.data_ptr(), kv_indices.data_ptr(), capacity)
+    _call("mla_block_table_to_shared_csr", index, stream, block_table.data_ptr(), seq_lens.data_ptr(), batch,
+          max_blocks, page_size, min_shared, group_indptr.data_ptr(), prefix_indptr.data_ptr(),
+          prefix_indices.data_ptr(), prefix_capacity, kv_indptr.data_ptr(), kv_indices.data_ptr(), capacity)
     return group_indptr, prefix_indptr, prefix_indices, kv_indptr, kv_indices

@@ -125,6 +125,9 @@ __global__ void __launch_bounds__(kScanThreads) groups_kernel(const SharedTableP
     if (g < n) p.prefix_indptr[g + 1] = offset32(end);
     run += total;
   }
+  // A row's group was written by another warp, after that warp's last meeting in the sum.
+  __threadfence_block();
+  __syncthreads();
   run = 0;
   for (int base = 0; base < n; base += kScanThreads) {
     const int i = base + threadIdx.x;

@@ -134,7 +134,9 @@ __global__ void __launch_bounds__(kScanThreads) groups_kernel(const SharedTableP
     long long keys = 0;
     if (i < n) {
       const int g = p.kv_indptr[i];
-      keys = length_of(p, i) - (__ldcg(p.prefix_indptr + g + 1) - __ldcg(p.prefix_indptr + g));
+      // (a length that was rewritten since the pages were counted may be the less: offsets never fall,
+      // so no list is written in front of its buffer)
+      keys = max(0LL, length_of(p, i) - (__ldcg(p.prefix_indptr + g + 1) - __ldcg(p.prefix_indptr + g)));
     }
     const long long end = run + scan_block(keys, part, &total);
     if (i < n) p.kv_indptr[i] = offset32(end - keys);

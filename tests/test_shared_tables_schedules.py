@@ -90,3 +90,13 @@ def test_lists_under_any_schedule(host, n, small, schedule):
         got = run(host, table, lens, page, min_shared, schedule, small, len(ref[4]) + 3, len(ref[2]) + 3)
         for have, want in zip(got, ref):
             assert have[:len(want)].tolist() == want and (have[len(want):] == FILL).all()
+
+
+@pytest.mark.parametrize("schedule", [0, 1])
+def test_lengths_that_change_meanwhile_lead_nowhere_else(host, schedule):
+    """Lengths rewritten between two launches of a call make lists that mean nothing, inside their buffers."""
+    rng = np.random.default_rng(5)
+    table, lens = make(rng, 70, 5, 2, 1.0)
+    table[:] = table[0]
+    lens[:] = 9
+    run(host, table, lens, 2, 1, schedule, False, 300, 50, later=rng.integers(0, 11, 70).astype(np.int32))

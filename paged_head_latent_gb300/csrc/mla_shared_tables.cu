@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kScanThreads) groups_kernel(const SharedTableP
   if (threadIdx.x == 0) p.kv_indptr[n] = offset32(run);
 }
 
-// Blocks (i, y): every kFillBlocks-th run of keys of row i's own list, and of group i's prefix.
+// Blocks (i, y): every kFillBlocks-th run of keys of row i's own list, and of group i's prefix.  The
+// offsets are read from L2: this kernel may have begun before they were written.
 __global__ void __launch_bounds__(kThreads) lists_kernel(const SharedTableParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the offsets
   const int lane = threadIdx.x & 31;
@@ -163,19 +164,19 @@ __global__ void __launch_bounds__(kThreads) lists_kernel(const SharedTableParams
     int g = 0;
     for (int n = p.batch; n > 1;) {
       const int s = (n + 31) / 32;
-      const bool below = lane * s < n && __ldg(p.group_indptr + g + lane * s) <= i;
+      const bool below = lane * s < n && __ldcg(p.group_indptr + g + lane * s) <= i;
       const int k = __popc(__ballot_sync(0xffffffffu, below));
       const int at = max(k - 1, 0) * s;
       g += at;
       n = min(s, n - at);
     }
-    const int shared = __ldg(p.prefix_indptr + g + 1) - __ldg(p.prefix_indptr + g);
-    fill(p.block_table + (size_t)i * p.max_blocks, shared, length_of(p, i) - shared, __ldg(p.kv_indptr + i),
+    const int shared = __ldcg(p.prefix_indptr + g + 1) - __ldcg(p.prefix_indptr + g);
+    fill(p.block_table + (size_t)i * p.max_blocks, shared, length_of(p, i) - shared, __ldcg(p.kv_indptr + i),
          p.kv_indices, p.capacity);
-    const int opens = __ldg(p.group_indptr + i), at = __ldg(p.prefix_indptr + i);
+    const int opens = __ldcg(p.group_indptr + i), at = __ldcg(p.prefix_indptr + i);
     if (opens < p.batch)
-      fill(p.block_table + (size_t)opens * p.max_blocks, 0, __ldg(p.prefix_indptr + i + 1) - at, at, p.prefix_indices,
-           p.prefix_capacity);
+      fill(p.block_table + (size_t)opens * p.max_blocks, 0, __ldcg(p.prefix_indptr + i + 1) - at, at,
+           p.prefix_indices, p.prefix_capacity);
   }
 }
 

@@ -4,6 +4,11 @@
 // so between two of them a warp may be as far ahead of the others as CUDA allows: the schedule
 // names which warp, and which lane of it, goes first.  A kernel whose result depends on the
 // schedule lacks a barrier.
+//
+// Loads.  __ldg is for what does not change while a kernel lives, and a kernel launched as a
+// programmatic dependent may live from before the launches in front of it: it may return what memory
+// held then.  So loads by __ldg from watched buffers, which those launches write, are counted
+// (early_loads).
 #pragma once
 #include <ucontext.h>
 
@@ -44,6 +49,8 @@ struct Machine {
   Fiber* now = nullptr;
   Dim3 block_idx, block_dim, grid_dim;
   std::function<void()> kernel;
+  std::vector<std::pair<const char*, const char*>> watched;
+  long long early_loads = 0;
 };
 inline Machine& machine() {
   static Machine m;
@@ -151,6 +158,14 @@ inline void run_block(Dim3 grid, Dim3 idx, int threads, unsigned schedule, std::
   }
 }
 
+inline void watch(const void* p, size_t bytes) {
+  machine().watched.emplace_back(static_cast<const char*>(p), static_cast<const char*>(p) + bytes);
+}
+inline void forget() {
+  machine().watched.clear();
+  machine().early_loads = 0;
+}
+
 }  // namespace host
 
 #define __global__
@@ -173,6 +188,8 @@ T __ldcg(const T* p) {
 }
 template <typename T>
 T __ldg(const T* p) {
+  const char* at = reinterpret_cast<const char*>(p);
+  for (auto& b : host::machine().watched) host::machine().early_loads += at >= b.first && at < b.second;
   return *p;
 }
 inline int atomicMin(int* p, int v) {

@@ -11,6 +11,9 @@ extern "C" {
 // as they are from the second launch on.  Returns 0, without the lists, if an offset could lead out of them.
 int tables_run(SharedTableParams* p, int small, unsigned schedule, const int32_t* later) {
   const size_t n = p->batch;
+  host::forget();
+  for (const int32_t* list : {(const int32_t*)p->group_indptr, (const int32_t*)p->prefix_indptr, (const int32_t*)p->kv_indptr})
+    host::watch(list, (n + 1) * 4);
   if (small) {
     host::run_block({1, 1, 1}, {0, 0, 0}, kScanThreads, schedule, [p] { small_tables_kernel(*p); });
     return 1;
@@ -28,5 +31,7 @@ int tables_run(SharedTableParams* p, int small, unsigned schedule, const int32_t
       host::run_block({rows, (unsigned)kFillBlocks, 1}, {i, y, 0}, kThreads, schedule, [p] { lists_kernel(*p); });
   return 1;
 }
+
+long long tables_early_loads() { return host::machine().early_loads; }
 
 }

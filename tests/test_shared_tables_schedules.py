@@ -1,5 +1,6 @@
 """The kernels that find shared prefixes, run from their source on the CPU under chosen schedules
-(cuda_on_host.h): their lists may not depend on which warp is ahead of which."""
+(cuda_on_host.h): their lists may not depend on which warp is ahead of which, nor on how early a kernel
+begins that overlaps the one whose offsets it reads."""
 
 import ctypes
 import os
@@ -46,7 +47,7 @@ def host(tmp_path_factory):
     subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-shared", "-fPIC", "-w", f"-I{ROOT}/tests",
                     f'-DKERNELS="{at}/kernels.h"', f"{ROOT}/tests/shared_tables_on_host.cpp", "-o", str(out)], check=True)
     lib = ctypes.CDLL(str(out))
-    lib.path = str(out)
+    lib.tables_early_loads.restype = ctypes.c_longlong
     return lib
 
 
@@ -62,6 +63,7 @@ def run(host, table, lens, page, min_shared, schedule, small, cap, pcap, later=N
     p = Params(table.ctypes.data, lens.ctypes.data, n, table.shape[1], page, min_shared, *at, pcap, cap)
     later = ctypes.c_void_p(later.ctypes.data if later is not None else None)
     assert host.tables_run(ctypes.byref(p), int(small), schedule, later), "an offset is negative or falls"
+    assert host.tables_early_loads() == 0, "offsets are read as if nothing wrote them while the kernel lives"
     for b, m in zip(bufs, (n + 1, n + 1, pcap, n + 1, cap)):
         assert (b[:GUARD] == FILL).all() and (b[GUARD + m:] == FILL).all()
     return [b[GUARD:len(b) - GUARD] for b in bufs]

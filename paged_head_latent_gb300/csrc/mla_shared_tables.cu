@@ -37,9 +37,10 @@ __global__ void __launch_bounds__(kThreads) common_pages_kernel(const SharedTabl
     const int32_t* a = p.block_table + (size_t)i * p.max_blocks;
     const int32_t* b = a - p.max_blocks;
     int differ = most;
+    // (unsigned: a step behind the last of 2^31 - 1 pages is not in front of the first)
 #pragma unroll 4
-    for (int k = threadIdx.x; k < most; k += kThreads)
-      if (__ldg(a + k) != __ldg(b + k)) differ = min(differ, k);
+    for (unsigned k = threadIdx.x; k < (unsigned)most; k += kThreads)
+      if (__ldg(a + k) != __ldg(b + k)) differ = min(differ, (int)k);
     differ = __reduce_min_sync(0xffffffffu, differ);
     if ((threadIdx.x & 31) == 0) first[threadIdx.x >> 5] = differ;
     __syncthreads();
@@ -150,13 +151,13 @@ __global__ void __launch_bounds__(kScanThreads) groups_kernel(const SharedTableP
 __global__ void __launch_bounds__(kThreads) lists_kernel(const SharedTableParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the offsets
   const int lane = threadIdx.x & 31;
-  const int first = blockIdx.y * kThreads + threadIdx.x, step = kThreads * gridDim.y;
+  const unsigned first = blockIdx.y * kThreads + threadIdx.x, step = kThreads * gridDim.y;
   auto fill = [&](const int32_t* row, int skip, long long n, int at, int32_t* list, long long room) {
-    n = min(n, room - at);
-    for (int k = first; k < n; k += step) {
-      const int key = skip + k;
+    const unsigned end = (unsigned)max(0LL, min(n, room - at));
+    for (unsigned k = first; k < end; k += step) {  // (unsigned, as above)
+      const int key = skip + (int)k;
       const long long slot = (long long)__ldg(row + key / p.page_size) * p.page_size + key % p.page_size;
-      list[at + k] = slot < 0 || slot > 0x7fffffffLL ? -1 : (int32_t)slot;
+      list[(size_t)at + k] = slot < 0 || slot > 0x7fffffffLL ? -1 : (int32_t)slot;
     }
   };
   for (int i = blockIdx.x; i < p.batch; i += gridDim.x) {

@@ -1,9 +1,30 @@
 // The kernels of the shared-prefix tables on the host (cuda_on_host.h).  KERNELS is their source with the
 // includes and the PTX taken out.
+#include <signal.h>
+#include <sys/mman.h>
+#include <unistd.h>
+
 #include "cuda_on_host.h"
 #include KERNELS
 
 using namespace mla;
+
+namespace {
+
+// n ints, all of which lie in the same 64 MB of memory, with nothing mapped for 8 GB on either side.
+int32_t* far_ints(size_t n) {
+  constexpr size_t kChunk = 64 << 20, kNothing = 9ull << 30;
+  const size_t bytes = (n * 4 + kChunk - 1) / kChunk * kChunk;
+  char* at = static_cast<char*>(
+      mmap(nullptr, bytes + 2 * kNothing, PROT_NONE, MAP_PRIVATE | MAP_ANONYMOUS | MAP_NORESERVE, -1, 0));
+  const int fd = memfd_create("ints", 0);
+  if (at == MAP_FAILED || fd < 0 || ftruncate(fd, kChunk) != 0) std::exit(4);
+  for (size_t o = 0; o < bytes; o += kChunk)
+    if (mmap(at + kNothing + o, kChunk, PROT_READ | PROT_WRITE, MAP_SHARED | MAP_FIXED, fd, 0) == MAP_FAILED) std::exit(4);
+  return reinterpret_cast<int32_t*>(at + kNothing);
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -29,6 +50,38 @@ int tables_run(SharedTableParams* p, int small, unsigned schedule, const int32_t
   for (unsigned i : host::order(rows, schedule, 2))
     for (unsigned y = 0; y < (unsigned)kFillBlocks; ++y)
       host::run_block({rows, (unsigned)kFillBlocks, 1}, {i, y, 0}, kThreads, schedule, [p] { lists_kernel(*p); });
+  return 1;
+}
+
+// Lists and rows of 2^31 - 1 entries, by the last warp of the last block.  Exits with 3 on an access outside of them.
+int tables_far(int what) {
+  signal(SIGSEGV, [](int) { _exit(3); });
+  constexpr int kMost = 0x7fffffff;
+  int32_t table[2] = {0, 0}, lens[2] = {kMost, kMost}, groups[3] = {0, 2, 2}, prefix[3] = {0, kMost, kMost}, own[3] = {0, 0, 0};
+  SharedTableParams p{table, lens, 2, 1, kMost, 1, groups, prefix, nullptr, own, nullptr, 0, 0};
+  const auto last_warp = [&](std::function<void()> kernel, unsigned x, unsigned y) {
+    host::run_block({2, (unsigned)kFillBlocks, 1}, {x, y, 0}, kThreads, 0, std::move(kernel), kThreads - 32, kThreads);
+  };
+  if (what == 0) {  // two rows of a page that both have in full: their prefix
+    p.prefix_indices = far_ints(kMost);
+    p.prefix_capacity = kMost;
+    last_warp([&] { lists_kernel(p); }, 0, kFillBlocks - 1);
+    return p.prefix_indices[kMost - 1] == kMost - 1;
+  }
+  if (what == 1) {  // a row's own keys
+    p.batch = 1;
+    groups[1] = 1;
+    prefix[1] = 0;
+    own[1] = kMost;
+    p.kv_indices = far_ints(kMost);
+    p.capacity = kMost;
+    last_warp([&] { lists_kernel(p); }, 0, kFillBlocks - 1);
+    return p.kv_indices[kMost - 1] == kMost - 1;
+  }
+  p.page_size = 1;  // rows of as many pages
+  p.max_blocks = kMost;
+  p.block_table = far_ints(2 * (size_t)kMost);
+  last_warp([&] { common_pages_kernel(p); }, 1, 0);
   return 1;
 }
 

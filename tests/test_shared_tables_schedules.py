@@ -7,6 +7,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -47,6 +48,7 @@ def host(tmp_path_factory):
     subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-shared", "-fPIC", "-w", f"-I{ROOT}/tests",
                     f'-DKERNELS="{at}/kernels.h"', f"{ROOT}/tests/shared_tables_on_host.cpp", "-o", str(out)], check=True)
     lib = ctypes.CDLL(str(out))
+    lib.path = str(out)
     lib.tables_early_loads.restype = ctypes.c_longlong
     return lib
 
@@ -102,3 +104,12 @@ def test_lengths_that_change_meanwhile_lead_nowhere_else(host, schedule):
     table[:] = table[0]
     lens[:] = 9
     run(host, table, lens, 2, 1, schedule, False, 300, 50, later=rng.integers(0, 11, 70).astype(np.int32))
+
+
+@pytest.mark.parametrize("what", ["prefix", "own keys", "pages"])
+def test_lists_as_long_as_an_int_counts(host, what):
+    """Counters that step past 2^31 - 1 end their loops there (in a process of its own: status 3 is an access
+    outside the list or the table)."""
+    n = ["prefix", "own keys", "pages"].index(what)
+    code = f"import ctypes, sys; sys.exit(0 if ctypes.CDLL({host.path!r}).tables_far({n}) == 1 else 1)"
+    assert subprocess.run([sys.executable, "-c", code]).returncode == 0

@@ -388,8 +388,8 @@ int mla_paged_prefill_shared_fp8(const void* q_nope, const void* q_pe, const voi
  * one for up to 64 rows with 65,536 keys at most (batch * max_blocks * page_size).
  * For a step with several new tokens per row call it after the pool has been extended: pages
  * with new tokens are never shared.
- * MLA_ERR_DIMS: negative sizes, page_size < 1, max_blocks * page_size or a capacity above
- * INT32_MAX.
+ * MLA_ERR_DIMS: negative sizes, page_size < 1, more than 2^30 rows, max_blocks * page_size or a
+ * capacity above INT32_MAX.
  */
 int mla_block_table_to_shared_csr(const int32_t* block_table, const int32_t* seq_lens, int batch, int max_blocks,
                                   int page_size, int min_shared, int32_t* group_indptr, int32_t* prefix_indptr,

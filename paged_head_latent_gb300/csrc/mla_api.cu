@@ -385,6 +385,7 @@ int mla_block_table_to_shared_csr(const int32_t* block_table, const int32_t* seq
                                   int32_t* prefix_indices, long long prefix_capacity, int32_t* kv_indptr,
                                   int32_t* kv_indices, long long capacity, void* stream) {
   if (batch < 0 || max_blocks < 0 || page_size < 1 || min_shared < 0) return MLA_ERR_DIMS;
+  if (batch > 1 << 30) return MLA_ERR_DIMS;  // (the kernels' counters of rows step past the batch)
   if (capacity < 0 || prefix_capacity < 0 || capacity > 0x7fffffffLL || prefix_capacity > 0x7fffffffLL)
     return MLA_ERR_DIMS;
   if ((long long)max_blocks * page_size > 0x7fffffffLL) return MLA_ERR_DIMS;

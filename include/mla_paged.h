@@ -343,9 +343,10 @@ int mla_paged_prefill_window_fp8(const void* q_nope, const void* q_pe, const voi
  *   dims->num_kv_indices, and up to 128 keys per group and request.  Staged keys of 2^31 or more are
  *   refused (MLA_ERR_DIMS; their workspace size reads 0).
  * Empty rows, rows behind the last request, slots outside the cache and keys that are not finite:
- * as for mla_paged_prefill_window.  MLA_VALIDATE checks both lists and the groups; as in the
- * other calls it reports lists that end short of their capacity, and for the prefill calls
- * requests with fewer own keys than new tokens, which are no error otherwise.
+ * as for mla_paged_prefill_window.  MLA_VALIDATE checks both lists and the groups, also where there
+ * is no group; as in the other calls it reports lists that end short of their capacity, and for
+ * the prefill calls requests with fewer own keys than new tokens, which are no error otherwise
+ * (nor are requests in no group, which it reports too).
  * The _fp8 calls read the FP8 cache of mla_paged_decode_fp8.
  */
 size_t mla_workspace_bytes_shared(const mla_dims* dims, int groups, int num_prefix_indices, int is_prefill);

@@ -501,7 +501,9 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
   const mla_dims* dims = &resolved;
   if (!std::isfinite(sm_scale)) return MLA_ERR_DIMS;
   if (dims->total_q == 0 || dims->batch == 0) return MLA_OK;
-  if (span.kind == mla::kShared && span.groups == 0) return MLA_OK;  // (no request is in a group)
+  // No request is in a group: no row is written, but MLA_VALIDATE reports requests that are left out.
+  const bool no_rows = span.kind == mla::kShared && span.groups == 0;
+  if (no_rows && !(flags & MLA_VALIDATE)) return MLA_OK;
   if (!q_nope || !q_pe || (!decode && !qo_indptr) || !kv_indptr || !out || !lse) return MLA_ERR_NULL;
   if (span.kind == mla::kShared && (!span.group_indptr || !span.prefix_indptr)) return MLA_ERR_NULL;
   if (span.num_prefix > 0 && !span.prefix_indices) return MLA_ERR_NULL;
@@ -604,6 +606,7 @@ int run_staged(const void* q_nope, const void* q_pe, const void* ckv_cache, cons
     if (mla::launch_validate(v, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
     if (span.kind == mla::kShared && mla::launch_validate_groups(p, stream) != cudaSuccess) return MLA_ERR_LAUNCH;
   }
+  if (no_rows) return MLA_OK;
   // Benchmark timing, as in run(): staging and attention, then the merge.
   std::unique_lock<std::mutex> prof_lk(g_prof_mu);
   cudaEvent_t* ev = profile_slot();

@@ -93,9 +93,9 @@ inline std::vector<int> order(int n, unsigned schedule, unsigned salt) {
   return v;
 }
 
-// Runs one block.  Threads outside [first, last) do not exist (for loops too long to run on all).
-inline void run_block(Dim3 grid, Dim3 idx, int threads, unsigned schedule, std::function<void()> kernel, int first = 0,
-                      int last = 1 << 30) {
+// Runs one block.  Threads in [absent, present) do not exist (for loops too long to run on all).
+inline void run_block(Dim3 grid, Dim3 idx, int threads, unsigned schedule, std::function<void()> kernel, int absent = 0,
+                      int present = 0) {
   Machine& m = machine();
   m.block_idx = idx;
   m.grid_dim = grid;
@@ -106,7 +106,7 @@ inline void run_block(Dim3 grid, Dim3 idx, int threads, unsigned schedule, std::
     Fiber& f = m.fibers[t];
     f.tid = Dim3{(unsigned)t, 0, 0};
     f.state = kDone;
-    if (t < first || t >= last) continue;
+    if (t >= absent && t < present) continue;
     constexpr size_t kStack = 64 << 10;
     if (!f.stack) f.stack.reset(new char[kStack]);
     getcontext(&f.ctx);

@@ -53,19 +53,20 @@ int tables_run(SharedTableParams* p, int small, unsigned schedule, const int32_t
   return 1;
 }
 
-// Lists and rows of 2^31 - 1 entries, by the last warp of the last block.  Exits with 3 on an access outside of them.
+// Lists and rows of 2^31 - 1 entries, by the first and the last warp of the last block.  Exits with 3 on an
+// access outside of them.
 int tables_far(int what) {
   signal(SIGSEGV, [](int) { _exit(3); });
   constexpr int kMost = 0x7fffffff;
   int32_t table[2] = {0, 0}, lens[2] = {kMost, kMost}, groups[3] = {0, 2, 2}, prefix[3] = {0, kMost, kMost}, own[3] = {0, 0, 0};
   SharedTableParams p{table, lens, 2, 1, kMost, 1, groups, prefix, nullptr, own, nullptr, 0, 0};
-  const auto last_warp = [&](std::function<void()> kernel, unsigned x, unsigned y) {
-    host::run_block({2, (unsigned)kFillBlocks, 1}, {x, y, 0}, kThreads, 0, std::move(kernel), kThreads - 32, kThreads);
+  const auto two_warps = [&](std::function<void()> kernel, unsigned x, unsigned y) {
+    host::run_block({2, (unsigned)kFillBlocks, 1}, {x, y, 0}, kThreads, 0, std::move(kernel), 32, kThreads - 32);
   };
   if (what == 0) {  // two rows of a page that both have in full: their prefix
     p.prefix_indices = far_ints(kMost);
     p.prefix_capacity = kMost;
-    last_warp([&] { lists_kernel(p); }, 0, kFillBlocks - 1);
+    two_warps([&] { lists_kernel(p); }, 0, kFillBlocks - 1);
     return p.prefix_indices[kMost - 1] == kMost - 1;
   }
   if (what == 1) {  // a row's own keys
@@ -75,13 +76,13 @@ int tables_far(int what) {
     own[1] = kMost;
     p.kv_indices = far_ints(kMost);
     p.capacity = kMost;
-    last_warp([&] { lists_kernel(p); }, 0, kFillBlocks - 1);
+    two_warps([&] { lists_kernel(p); }, 0, kFillBlocks - 1);
     return p.kv_indices[kMost - 1] == kMost - 1;
   }
   p.page_size = 1;  // rows of as many pages
   p.max_blocks = kMost;
   p.block_table = far_ints(2 * (size_t)kMost);
-  last_warp([&] { common_pages_kernel(p); }, 1, 0);
+  two_warps([&] { common_pages_kernel(p); }, 1, 0);
   return 1;
 }
 

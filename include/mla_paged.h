@@ -385,8 +385,11 @@ int mla_paged_prefill_shared_fp8(const void* q_nope, const void* q_pe, const voi
  *   kv_indptr [batch + 1], kv_indices [capacity]: every row's keys behind the shared ones
  * Slots as for mla_block_table_to_csr (-1 where they do not fit an int32).  Entries at or past a
  * capacity, and behind the end of a list, are left as they were; the offsets still count
- * entries past the capacity, and stay at 2^31 - 1 once they have reached it.  Three launches, or
- * one for up to 64 rows with 65,536 keys at most (batch * max_blocks * page_size).
+ * entries past the capacity, and stay at 2^31 - 1 once they have reached it.  (The attention takes
+ * keys past num_prefix_indices or num_kv_indices for none; MLA_VALIDATE reports them.)  Three
+ * launches, or one for up to 64 rows with 65,536 keys at most (batch * max_blocks * page_size).
+ * Lists of less than the table's room are what keeps the attention's workspace small; min_shared is
+ * what keeps prefixes that are too short to pay out of the groups.
  * For a step with several new tokens per row call it after the pool has been extended: pages
  * with new tokens are never shared.
  * MLA_ERR_DIMS: negative sizes, page_size < 1, more than 2^30 rows, max_blocks * page_size or a

@@ -32,7 +32,10 @@ struct ChunkBlock {
   int tiles;     // key tiles that its rows see (at least 1)
   int tile0;     // kCausal: first staged tile of the request; else the staged row of the first run
   int seen;      // keys that token 0 of the request sees (may be <= 0; kShared: unused)
-  int halves;    // halves (at most 2 * tiles, at least one less; causal: unused, as what follows)
+  // Halves: at most 2 * tiles, at least one less; but 0 for rows that see no key, which walk a tile all
+  // the same (kWindow: the request's first half, masked; kShared: the half of zeros).  Causal: unused,
+  // as what follows.
+  int halves;
   int head;      // ... of the first run
   int rest0;     // staged row of the second run
   int rest_key;  // kWindow: ... and its first key's number in the request

@@ -28,8 +28,9 @@
 // What bounds it.  A tile takes 2470 cycles with its share of the blocks' starts and ends (four
 // prompts, 128 heads, 22 tiles a block: 850 to 870 us with staging and merge, 1.72 to 1.76 PFLOP/s,
 // 0.90 to 0.92 of the measured bf16 burst rate, at the 1.6 GHz that the power limit leaves; one
-// prompt of 256 tokens over 4096 keys: tensor pipe 80 % active).  What writes shared memory, the loads and P, is 152 KB a tile, 1216 cycles at 128
-// bytes a cycle; the products read their operands besides, at a rate that was not measured.
+// prompt of 256 tokens over 4096 keys: tensor pipe 80 % active).  What writes shared memory, the
+// loads and P, is 152 KB a tile, 1216 cycles at 128 bytes a cycle; the products read their operands
+// besides, at a rate that was not measured.
 //
 // The window and the shared attention (kSpan; decode calls of theirs too) take the same tiles as
 // pairs of halves of 64 keys, each from one of two runs (chunk.h), so that a window begins and a
@@ -39,7 +40,7 @@
 // windows and lists have many of).  Measured at the power limit, with staging: 2710 tokens of 128
 // heads with windows of 1024 keys 583 us (1.29 PFLOP/s), 1374 tokens of 128 heads behind two prefixes of
 // 1408 keys 448 us (1.42).  64 requests x 128 heads, windows of 4096 keys in 64-key pages: 82 us, DRAM at
-// 4.7 to 4.9 TB/s in the kernel, which starts and ends with no load in flight.
+// 5.0 TB/s in the kernel, which starts and ends with no load in flight.
 //
 // The tensor pipe's order is S(j+1), then O += P(j) V(j): the softmax of tile j runs while S(j+1)
 // is computed.
@@ -47,6 +48,10 @@
 // Warps: 0-7 softmax and output (a thread has a row, a quarter of a tile's keys and a quarter of
 // the output's columns), 8 loads Q and K, 9 loads V, 10 issues the products (leader SM only), 11
 // tensor memory.
+//
+// Two rules of the waits.  The warp that issues the products waits as a whole and stays converged.
+// And a wait by parity may be one phase behind its barrier at most (the phase before has the parity
+// of the one to come), so a warp waits for every phase of a barrier that it uses, needed or not.
 #include <mutex>
 
 #include "chunk.h"
@@ -188,8 +193,9 @@ struct Walk {
 };
 
 // ---- the window and the shared attention: a tile's two halves of 64 keys
-// Staged row of half h of the tile that a walk stands at (of an odd block's last tile: of a half that
-// may be loaded).
+// Staged row of half h of the tile that a walk stands at.  An odd block's last tile has one half, but
+// loads two and takes S of both (kWindow: its last half again, kShared: the half of zeros); only
+// their P V is left out.
 template <int kSpan>
 __device__ __forceinline__ int half_row(const ChunkParams& p, const Walk& it, int h) {
   int u = 2 * it.t + h;

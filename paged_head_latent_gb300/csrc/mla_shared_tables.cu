@@ -11,8 +11,9 @@
 // list i: the slots behind them of row i.  Integer work, whose outcome is unique.
 //
 // What bounds it: latency.  The first launch reads the table once (a block a row), the second is
-// one block's four scans, the third writes the lists: 15 us in a graph for 500 rows of up to 290
-// pages, 4, 5 and 10 us by themselves.  A small table takes one block and one launch: 8 us for 16 rows of 60 pages.
+// one block's three scans (groups, prefix offsets, own offsets), the third writes the lists: 4, 5
+// and 10 us by themselves for 500 rows of up to 290 pages.  A small table takes one block and one
+// launch: 8 us for 16 rows of 60 pages.
 #include "launch.h"
 
 namespace mla {

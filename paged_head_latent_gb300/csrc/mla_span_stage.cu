@@ -369,7 +369,9 @@ __device__ __forceinline__ bool shared_source(const ChunkParams& p, const OwnTab
   s->end = r.kv_len;
   s->from = at * kHalfKeys + row % kHalfKeys;
   s->info = HalfInfo{r.q0, r.q0 + r.q_len, seen - r.q0 - at * kHalfKeys, 0};
-  // A block may have rows of several requests, if it is not filled by a token.
+  // A block may have rows of several requests, if it is not filled by a token: then their own keys are
+  // staged, as a key that is not finite must not reach the others' rows.  (64 requests of 4000 own
+  // keys behind prefixes of 64, in 64-key pages: 173 us with 16 heads, 87 with 128, read in place.)
   s->direct = (at + 1) * kHalfKeys <= seen;
   if (s->direct && p.sources && p.heads != kChunkRows) {
     const int g = owner_of(p.groups, b, [&](int i) { return clamped(p.group_indptr, i, p.batch); });

@@ -177,7 +177,8 @@ def mla_paged_decode_shared(q_nope, q_pe, ckv_cache, kpe_cache, group_indptr, pr
                             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """One query token per request over the keys that its group shares (``prefix_*``) and those of
     its own (``kv_*``).  Group g: requests group_indptr[g] .. group_indptr[g + 1] - 1;
-    ``block_table_to_shared_csr`` makes all five lists.  Returns (out, lse)."""
+    ``block_table_to_shared_csr`` makes all five lists.  Rows of requests in no group are not
+    written, neither in ``out`` and ``lse`` as given nor in new ones.  Returns (out, lse)."""
     return _shared("mla_paged_decode_shared", q_nope, q_pe, (ckv_cache, kpe_cache), None, group_indptr,
                    prefix_indptr, prefix_indices, kv_indptr, kv_indices, sm_scale, out, lse, workspace, flags,
                    num_workers, stream)
@@ -195,7 +196,8 @@ def mla_paged_prefill_shared(q_nope, q_pe, ckv_cache, kpe_cache, qo_indptr, grou
                              kv_indptr, kv_indices, sm_scale, out=None, lse=None, workspace=None, flags=0,
                              num_workers=0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Ragged chunks of new tokens behind a shared prefix: every token sees the whole prefix of
-    its group, and causally the keys of its own request (``kv_*``: the new tokens' among them)."""
+    its group, and causally the keys of its own request (``kv_*``: the new tokens' among them).
+    Rows of requests in no group are not written."""
     return _shared("mla_paged_prefill_shared", q_nope, q_pe, (ckv_cache, kpe_cache), qo_indptr,
                    group_indptr, prefix_indptr, prefix_indices, kv_indptr, kv_indices, sm_scale, out, lse, workspace,
                    flags, num_workers, stream)
@@ -230,7 +232,8 @@ def block_table_to_shared_csr(block_table, seq_lens, page_size, min_shared=1, pr
     they share at least ``min_shared`` keys (and one page).  Returns (group_indptr [batch + 1],
     prefix_indptr [batch + 1], prefix_indices [prefix_capacity], kv_indptr [batch + 1], kv_indices
     [capacity]), which ``mla_paged_decode_shared`` takes as they are.  The capacities default to what
-    the table can name; entries behind the end of a list are left as they were."""
+    the table can name, and the attention's workspace follows them (1152 bytes an entry): smaller
+    ones are fine where the lists fit.  Entries behind the end of a list are left as they were."""
     _check("block_table", block_table, _I32)
     index = block_table.get_device()
     _check("seq_lens", seq_lens, _I32, index)

@@ -45,7 +45,7 @@ def host(tmp_path_factory):
     at = tmp_path_factory.mktemp("host")
     (at / "kernels.h").write_text(kernels())
     out = at / "tables.so"
-    subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-shared", "-fPIC", "-w", f"-I{ROOT}/tests",
+    subprocess.run(["g++", "-std=c++17", "-O2", "-fwrapv", "-shared", "-fPIC", "-w", f"-I{ROOT}/tests",
                     f'-DKERNELS="{at}/kernels.h"', f"{ROOT}/tests/shared_tables_on_host.cpp", "-o", str(out)], check=True)
     lib = ctypes.CDLL(str(out))
     lib.path = str(out)

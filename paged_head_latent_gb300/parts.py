@@ -215,6 +215,8 @@ def mla_paged_prefill_shared_fp8(q_nope, q_pe, kv_fp8, qo_indptr, group_indptr, 
 # ---------------------------------------------------------------- the groups of a batch
 def _room(name, capacity, t, most):
     if t is not None:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != 1 or (capacity is not None and t.shape[0] != capacity):
             raise ValueError(f"{name} must be [capacity]")
         return t.shape[0]

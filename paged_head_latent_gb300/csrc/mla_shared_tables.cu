@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kScanThreads) small_tables_kernel(const Shared
     }
     for (int i = g + 1; i <= n; ++i) opens[i] = n, prefix[i] = at;
     for (int i = 0; i < n; ++i) {
-      const int keys = own[i] - (prefix[group[i] + 1] - prefix[group[i]]);
+      const int keys = max(0, own[i] - (prefix[group[i] + 1] - prefix[group[i]]));  // (as in groups_kernel)
       own[i] = next;
       next += keys;
     }

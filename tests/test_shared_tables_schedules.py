@@ -16,7 +16,7 @@ from tests.conftest import ROOT
 from tests.test_shared_tables import groups_of
 
 CSRC = os.path.join(ROOT, "paged_head_latent_gb300", "csrc")
-FILL, GUARD = -77, 64
+FILL, GUARD = -77, 1024
 
 
 class Params(ctypes.Structure):
@@ -97,13 +97,16 @@ def test_lists_under_any_schedule(host, n, small, schedule):
 
 
 @pytest.mark.parametrize("schedule", [0, 1])
-def test_lengths_that_change_meanwhile_lead_nowhere_else(host, schedule):
-    """Lengths rewritten between two launches of a call make lists that mean nothing, inside their buffers."""
+@pytest.mark.parametrize("n,small", [(70, False), (50, True)])
+def test_lengths_that_change_meanwhile_lead_nowhere_else(host, n, small, schedule):
+    """Lengths rewritten between two launches of a call, or during its single one, make lists that mean nothing, inside
+    their buffers."""
     rng = np.random.default_rng(5)
-    table, lens = make(rng, 70, 5, 2, 1.0)
+    table, lens = make(rng, n, 5, 2, 1.0)
     table[:] = table[0]
     lens[:] = 9
-    run(host, table, lens, 2, 1, schedule, False, 300, 50, later=rng.integers(0, 11, 70).astype(np.int32))
+    run(host, table, lens, 2, 1, schedule, small, 300, 50, later=rng.integers(0, 11, n).astype(np.int32))
+    run(host, table, lens, 2, 1, schedule, small, 300, 50, later=np.zeros(n, np.int32))
 
 
 @pytest.mark.parametrize("what", ["prefix", "own keys", "pages"])
